@@ -14,6 +14,9 @@
 #include <string>
 
 #include "sk_internal.cuh"
+#include "sk_loss.cuh"
+#include "sk_lut8.cuh"
+#include "sk_norm.cuh"
 #include "sk_sketch.cuh"
 
 namespace {
@@ -139,6 +142,15 @@ bool routed_dx_possible(int64_t n, int64_t d, int64_t T, int ntask) {
   return forced == 2 || T >= kBwdTcMinT;
 }
 
+// LUT gradient from a checkpoint: the same rules as the bf16 tensor-core
+// backward, for one LUT set and for several.
+bool use_tensor_cores_lut8(int64_t n, int64_t d, int64_t T, int ntask) {
+  if (ntask > sk::kMaxRouteTasks || n < 64 || d < 64) return false;
+  const int forced = env_path("SK_BWD_PATH");
+  if (forced == 1) return false;
+  return forced == 2 || T >= kBwdTcMinT;
+}
+
 // Shape rules shared by the layer calls.
 sk_status check_shape(int bits, int gpr, int64_t n, int64_t d, int64_t T, int ntask) {
   if (bits < 2 || bits > 4) return fail(SK_ERR_INVALID_ARG, "bits must be 2, 3 or 4 (got %d)", bits);
@@ -255,7 +267,7 @@ sk_status sk_dequant(const void* packed, const uint16_t* lut, int bits, int gpr,
 }
 
 size_t sk_workspace_bytes(int op, int64_t n, int64_t d, int bits, int gpr, int64_t T, int ntask) {
-  if (op < SK_OP_FWD || op > SK_OP_BWD_LUT) return 0;
+  if (op < SK_OP_FWD || op > SK_OP_BWD_LUT_CKPT8) return 0;
   if (bits < 2 || bits > 4 || n < 1 || d < 32 || gpr < 1 || d % gpr != 0 || T < 1) return 0;
   if (op == SK_OP_BWD_LUT && use_tensor_cores_bwd(n, d, T, ntask))
     return sk::dlut_tc_workspace(n, d, bits, gpr);
@@ -263,6 +275,8 @@ size_t sk_workspace_bytes(int op, int64_t n, int64_t d, int bits, int gpr, int64
   if (op == SK_OP_BWD_INPUT && routed_dx_possible(n, d, T, ntask)) return sk::dx_tc_workspace(T, n, ntask);
   if (op == SK_OP_BWD_LUT && routed_dx_possible(n, d, T, ntask))
     return sk::dlut_tc_routed_workspace(n, d, bits, gpr, T, ntask);
+  if (op == SK_OP_BWD_LUT_CKPT8 && use_tensor_cores_lut8(n, d, T, ntask))
+    return sk::lut8_tc_workspace(n, d, bits, gpr, T, ntask, ntask > 1);
   return 0;
 }
 
@@ -504,6 +518,257 @@ sk_status sk_linear_bwd_lut_noalloc(const void* packed, int bits, int gpr, int64
     e = sk::launch_simt_bwd_lut(p, X, dY, dlut, accumulate, s);
   }
   return e == cudaSuccess ? ok() : cuda_fail(e, "LUT-gradient kernel launch");
+}
+
+// Shape rules of the checkpoint calls.
+static sk_status check_ckpt8(int64_t T, int64_t d) {
+  if (d < 32 || d % 32 != 0 || d >= kMaxDim) return fail(SK_ERR_INVALID_ARG, "d must be a positive multiple of 32 below 2^31 (got %lld)", (long long)d);
+  if (T < 0 || T >= kMaxDim) return fail(SK_ERR_INVALID_ARG, "T must be in [0, 2^31) (got %lld)", (long long)T);
+  return SK_OK;
+}
+
+static sk_status ckpt8_buffers(const uint16_t* X, const int8_t* q, const uint8_t* scale, int64_t T, int64_t d) {
+  if (!X || !q || !scale) return fail(SK_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(X) || !aligned16(q) || !aligned16(scale)) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  const size_t xb = (size_t)(T * d) * 2, qb = (size_t)(T * d), sb = (size_t)(T * (d / 32));
+  if (overlaps(X, xb, q, qb) || overlaps(X, xb, scale, sb) || overlaps(q, qb, scale, sb))
+    return fail(SK_ERR_INVALID_ARG, "buffers overlap");
+  return SK_OK;
+}
+
+sk_status sk_ckpt8_quantize(const uint16_t* X, int64_t T, int64_t d, int8_t* q, uint8_t* scale, sk_stream_t stream) {
+  g_last_error.clear();
+  sk_status st = check_ckpt8(T, d);
+  if (st != SK_OK) return st;
+  if (T == 0) return ok();
+  st = ckpt8_buffers(X, q, scale, T, d);
+  if (st != SK_OK) return st;
+  unsigned int* check = nullptr;
+  st = device_state(&check);
+  if (st != SK_OK) return st;
+  cudaError_t e = sk::launch_ckpt8_quantize(X, T, d, q, scale, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "checkpoint kernel launch");
+}
+
+sk_status sk_ckpt8_dequantize(const int8_t* q, const uint8_t* scale, int64_t T, int64_t d, uint16_t* X,
+                              sk_stream_t stream) {
+  g_last_error.clear();
+  sk_status st = check_ckpt8(T, d);
+  if (st != SK_OK) return st;
+  if (T == 0) return ok();
+  st = ckpt8_buffers(X, q, scale, T, d);
+  if (st != SK_OK) return st;
+  unsigned int* check = nullptr;
+  st = device_state(&check);
+  if (st != SK_OK) return st;
+  cudaError_t e = sk::launch_ckpt8_dequantize(q, scale, T, d, X, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "checkpoint kernel launch");
+}
+
+sk_status sk_linear_bwd_lut_ckpt8(const void* packed, int bits, int gpr, int64_t n, int64_t d, const int8_t* q,
+                                  const uint8_t* scale, const uint16_t* dY, int64_t T, const int32_t* task, int ntask,
+                                  float* dlut, int accumulate, void* workspace, size_t workspace_bytes,
+                                  sk_stream_t stream) {
+  g_last_error.clear();
+  sk_status st = check_shape(bits, gpr, n, d, T, ntask);
+  if (st != SK_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return fail(SK_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+  const size_t dlut_bytes = (size_t)ntask * n * gpr * (1u << bits) * 4;
+  if (!dlut) return fail(SK_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(dlut)) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (T == 0) {
+    if (accumulate) return ok();
+    cudaError_t e = cudaMemsetAsync(dlut, 0, dlut_bytes, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "cudaMemsetAsync(dlut)");
+  }
+  const size_t qb = (size_t)(T * d), sb = (size_t)(T * (d / 32)), yb = (size_t)(T * n * 2);
+  st = check_layer_buffers(packed, nullptr, false, bits, gpr, n, d, T, task, ntask, q, qb, dY, yb, dlut, dlut_bytes);
+  if (st != SK_OK) return st;
+  if (!scale) return fail(SK_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(scale)) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (overlaps(dlut, dlut_bytes, scale, sb)) return fail(SK_ERR_INVALID_ARG, "output overlaps an input");
+  const size_t need = sk_workspace_bytes(SK_OP_BWD_LUT_CKPT8, n, d, bits, gpr, T, ntask);
+  if (need) {
+    if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))
+      return fail(SK_ERR_INVALID_ARG, "workspace of %zu bytes (16-byte aligned) required", need);
+    if (overlaps(workspace, need, q, qb) || overlaps(workspace, need, scale, sb) || overlaps(workspace, need, dY, yb) ||
+        overlaps(workspace, need, dlut, dlut_bytes) || overlaps(workspace, need, packed, sk_packed_bytes(n, d, bits)) ||
+        overlaps(workspace, need, task, task ? (size_t)T * 4 : 0))
+      return fail(SK_ERR_INVALID_ARG, "workspace overlaps another buffer");
+  }
+  unsigned int* check = nullptr;
+  st = device_state(&check);
+  if (st != SK_OK) return st;
+  sk::Problem p = make_problem(packed, nullptr, bits, gpr, n, d, T, task, ntask, check);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = use_tensor_cores_lut8(n, d, T, ntask)
+                      ? sk::launch_lut8_tc(p, q, scale, dY, dlut, accumulate, task != nullptr && ntask > 1, workspace, s)
+                      : sk::launch_lut8_simt(p, q, scale, dY, dlut, accumulate, s);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "LUT-gradient kernel launch");
+}
+
+// Element size of a norm type, 0 if it is none.
+static size_t type_bytes(int t) { return t == SK_F32 ? 4 : t == SK_BF16 || t == SK_F16 ? 2 : 0; }
+
+static sk_status check_norm(int xtype, int wtype, int64_t T, int64_t d, int rms) {
+  if (!type_bytes(xtype)) return fail(SK_ERR_INVALID_ARG, "unknown element type %d", xtype);
+  if (wtype != xtype && wtype != SK_F32) return fail(SK_ERR_INVALID_ARG, "the weight must have the rows' type or fp32 (got %d)", wtype);
+  if (d < 1 || d > sk::kNormMaxD) return fail(SK_ERR_INVALID_ARG, "d must be in [1, %lld] (got %lld)", (long long)sk::kNormMaxD, (long long)d);
+  if (T < 0 || T >= kMaxDim) return fail(SK_ERR_INVALID_ARG, "T must be in [0, 2^31) (got %lld)", (long long)T);
+  if (rms != 0 && rms != 1) return fail(SK_ERR_INVALID_ARG, "rms must be 0 or 1");
+  return SK_OK;
+}
+
+struct Buffer {
+  const void* p;
+  size_t bytes;
+};
+
+// Every output against every input and every other output; NULLs are absent.
+static sk_status check_buffers(const Buffer* in, int nin, const Buffer* out, int nout) {
+  for (int a = 0; a < nin; ++a)
+    if (in[a].p && !aligned16(in[a].p)) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  for (int a = 0; a < nout; ++a) {
+    if (!out[a].p) continue;
+    if (!aligned16(out[a].p)) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+    for (int b = 0; b < nin; ++b)
+      if (overlaps(out[a].p, out[a].bytes, in[b].p, in[b].bytes)) return fail(SK_ERR_INVALID_ARG, "output overlaps an input");
+    for (int b = 0; b < a; ++b)
+      if (overlaps(out[a].p, out[a].bytes, out[b].p, out[b].bytes)) return fail(SK_ERR_INVALID_ARG, "outputs overlap");
+  }
+  return SK_OK;
+}
+
+size_t sk_layer_norm_bwd_workspace_bytes(int64_t T, int64_t d) {
+  if (T < 1 || d < 1 || d > sk::kNormMaxD) return 0;
+  return (size_t)sk::norm_bwd_parts(T, d) * 2 * d * 4;
+}
+
+sk_status sk_layer_norm_fwd(const void* x, int xtype, int64_t T, int64_t d, const void* w, const void* b, int wtype,
+                            float eps, int rms, void* y, float* mean, float* rstd, int8_t* q, uint8_t* scale,
+                            sk_stream_t stream) {
+  g_last_error.clear();
+  sk_status st = check_norm(xtype, wtype, T, d, rms);
+  if (st != SK_OK) return st;
+  if (!(eps >= 0.f && std::isfinite(eps))) return fail(SK_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if ((q == nullptr) != (scale == nullptr)) return fail(SK_ERR_INVALID_ARG, "q and scale go together");
+  if (q && (xtype != SK_BF16 || d % 32 != 0))
+    return fail(SK_ERR_INVALID_ARG, "a checkpoint needs bf16 rows whose length is a multiple of 32");
+  if (T == 0) return ok();
+  if (!x || !w || !y) return fail(SK_ERR_INVALID_ARG, "null pointer");
+  const size_t xb = (size_t)(T * d) * type_bytes(xtype), wb = (size_t)d * type_bytes(wtype);
+  const Buffer in[] = {{x, xb}, {w, wb}, {b, wb}};
+  const Buffer out[] = {{y, xb}, {mean, (size_t)T * 4}, {rstd, (size_t)T * 4}, {q, (size_t)(T * d)}, {scale, (size_t)(T * (d / 32))}};
+  st = check_buffers(in, 3, out, 5);
+  if (st != SK_OK) return st;
+  unsigned int* check = nullptr;
+  st = device_state(&check);
+  if (st != SK_OK) return st;
+  sk::NormFwd a{x, w, b, y, mean, rstd, q, scale, T, d, eps, rms, xtype, wtype};
+  cudaError_t e = sk::launch_norm_fwd(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "norm kernel launch");
+}
+
+sk_status sk_layer_norm_bwd(const void* dy, const void* x, int xtype, int64_t T, int64_t d, const void* w, int wtype,
+                            const float* mean, const float* rstd, int rms, void* dx, void* dw, void* db,
+                            void* workspace, size_t workspace_bytes, sk_stream_t stream) {
+  g_last_error.clear();
+  sk_status st = check_norm(xtype, wtype, T, d, rms);
+  if (st != SK_OK) return st;
+  const size_t xb = (size_t)(T * d) * type_bytes(xtype), wb = (size_t)d * type_bytes(wtype);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    for (void* o : {dw, db}) {
+      if (!o) continue;
+      cudaError_t e = cudaMemsetAsync(o, 0, wb, s);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    }
+    return ok();
+  }
+  if (!dy || !x || !w || !rstd || (!mean && !rms)) return fail(SK_ERR_INVALID_ARG, "null pointer");
+  if (!dx && !dw && !db) return ok();
+  const size_t need = dw || db ? sk_layer_norm_bwd_workspace_bytes(T, d) : 0;
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(SK_ERR_INVALID_ARG, "workspace of %zu bytes (16-byte aligned) required", need);
+  const Buffer in[] = {{dy, xb}, {x, xb}, {w, wb}, {mean, (size_t)T * 4}, {rstd, (size_t)T * 4}};
+  const Buffer out[] = {{dx, xb}, {dw, wb}, {db, wb}, {need ? workspace : nullptr, need}};
+  st = check_buffers(in, 5, out, 4);
+  if (st != SK_OK) return st;
+  unsigned int* check = nullptr;
+  st = device_state(&check);
+  if (st != SK_OK) return st;
+  sk::NormBwd a{dy, x, w, mean, rstd, dx, dw, db, static_cast<float*>(workspace), T, d, rms, xtype, wtype};
+  cudaError_t e = sk::launch_norm_bwd(a, s);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "norm kernel launch");
+}
+
+static sk_status check_ce(int64_t T, int64_t V, int64_t d) {
+  if (T < 0 || T >= kMaxDim) return fail(SK_ERR_INVALID_ARG, "T must be in [0, 2^31) (got %lld)", (long long)T);
+  if (V < 1 || V >= (int64_t(1) << 24)) return fail(SK_ERR_INVALID_ARG, "V must be in [1, 2^24) (got %lld)", (long long)V);
+  if (d < 8 || d % 8 != 0 || d >= (int64_t(1) << 20))
+    return fail(SK_ERR_INVALID_ARG, "d must be a positive multiple of 8 below 2^20 (got %lld)", (long long)d);
+  return SK_OK;
+}
+
+size_t sk_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t d, int want_dh, int want_dw) {
+  if (T < 1 || T >= kMaxDim || V < 1 || V >= (int64_t(1) << 24) || d < 8 || d % 8 != 0 || d >= (int64_t(1) << 20)) return 0;
+  return sk::cross_entropy_workspace(T, V, d, want_dh != 0, want_dw != 0);
+}
+
+sk_status sk_cross_entropy(const uint16_t* H, const uint16_t* W, const void* target, int target_bits, int64_t T,
+                           int64_t V, int64_t d, int64_t ignore_index, int reduction, const float* dloss, float* loss,
+                           uint16_t* dH, uint16_t* dW, void* workspace, size_t workspace_bytes, sk_stream_t stream) {
+  g_last_error.clear();
+  sk_status st = check_ce(T, V, d);
+  if (st != SK_OK) return st;
+  if (target_bits != 32 && target_bits != 64) return fail(SK_ERR_INVALID_ARG, "target_bits must be 32 or 64 (got %d)", target_bits);
+  if (reduction < SK_CE_NONE || reduction > SK_CE_SUM) return fail(SK_ERR_INVALID_ARG, "unknown reduction %d", reduction);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    cudaError_t e = cudaSuccess;
+    if (loss && reduction != SK_CE_NONE) e = cudaMemsetAsync(loss, 0, 4, s);
+    if (e == cudaSuccess && dW) e = cudaMemsetAsync(dW, 0, (size_t)(V * d) * 2, s);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "cudaMemsetAsync");
+  }
+  if (!loss && !dH && !dW) return ok();
+  if (!H || !W || !target) return fail(SK_ERR_INVALID_ARG, "null pointer");
+  const size_t need = sk_cross_entropy_workspace_bytes(T, V, d, dH != nullptr, dW != nullptr);
+  if (!workspace || workspace_bytes < need)
+    return fail(SK_ERR_INVALID_ARG, "workspace of %zu bytes (16-byte aligned) required", need);
+  const size_t hb = (size_t)(T * d) * 2, wb = (size_t)(V * d) * 2;
+  const size_t lb = reduction == SK_CE_NONE ? (size_t)T * 4 : 4;
+  const Buffer in[] = {{H, hb}, {W, wb}, {target, (size_t)T * (target_bits / 8)}, {dloss, lb}};
+  const Buffer out[] = {{loss, lb}, {dH, hb}, {dW, wb}, {workspace, need}};
+  for (const Buffer& b : in)                    // a single value needs no more than its own alignment
+    if (b.p && !aligned16(b.p) && b.p != dloss) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  for (int a = 0; a < 4; ++a) {
+    if (!out[a].p) continue;
+    if (!aligned16(out[a].p) && out[a].p != loss) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+    for (const Buffer& b : in)
+      if (overlaps(out[a].p, out[a].bytes, b.p, b.bytes)) return fail(SK_ERR_INVALID_ARG, "output overlaps an input");
+    for (int b = 0; b < a; ++b)
+      if (overlaps(out[a].p, out[a].bytes, out[b].p, out[b].bytes)) return fail(SK_ERR_INVALID_ARG, "outputs overlap");
+  }
+  unsigned int* check = nullptr;
+  st = device_state(&check);
+  if (st != SK_OK) return st;
+  sk::CrossEntropy a{H, W, target, target_bits == 64, T, V, d, ignore_index, reduction, dloss, loss, dH, dW, workspace, check};
+  cudaError_t e = sk::launch_cross_entropy(a, s);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "cross-entropy kernel launch");
+}
+
+sk_status sk_scale_bf16(uint16_t* x, int64_t count, const float* factor, sk_stream_t stream) {
+  g_last_error.clear();
+  if (count < 0 || count % 8 != 0) return fail(SK_ERR_INVALID_ARG, "count must be a multiple of 8 (got %lld)", (long long)count);
+  if (count == 0) return ok();
+  if (!x || !factor) return fail(SK_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x)) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (overlaps(x, (size_t)count * 2, factor, 4)) return fail(SK_ERR_INVALID_ARG, "output overlaps an input");
+  unsigned int* check = nullptr;
+  sk_status st = device_state(&check);
+  if (st != SK_OK) return st;
+  cudaError_t e = sk::launch_scale_bf16(x, count, factor, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "scale kernel launch");
 }
 
 sk_status sk_bin_counts(const void* packed, int bits, int gpr, int64_t n, int64_t d, int32_t* counts,

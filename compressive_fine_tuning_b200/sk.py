@@ -7,21 +7,25 @@ fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsk.so")
 
 SK_OK = 0
-SK_OP_FWD, SK_OP_BWD_INPUT, SK_OP_BWD_LUT = 0, 1, 2
+SK_OP_FWD, SK_OP_BWD_INPUT, SK_OP_BWD_LUT, SK_OP_BWD_LUT_CKPT8 = 0, 1, 2, 3
+SK_F32, SK_BF16, SK_F16 = 0, 1, 2
+SK_CE_NONE, SK_CE_MEAN, SK_CE_SUM = 0, 1, 2
 SK_CHECK_TASK_RANGE = 1
 SK_CHECK_INDEX_RANGE = 2
 SK_CHECK_TIMEOUT = 4
 SK_CHECK_NOT_SPD = 8
 SK_CHECK_LUT_ORDER = 16
+SK_CHECK_TARGET_RANGE = 32
 
 EXPORTED = (
     "sk_abi_version", "sk_status_string", "sk_last_error", "sk_packed_row_bytes", "sk_packed_bytes",
@@ -30,6 +34,9 @@ EXPORTED = (
     "sk_linear_bwd_lut", "sk_linear_bwd_lut_noalloc", "sk_bin_counts", "sk_lut_adamw", "sk_lut_sgd",
     "sk_device_check", "sk_inverse_factor_workspace_bytes", "sk_sketch_round_workspace_bytes", "sk_gram",
     "sk_inverse_factor", "sk_lloyd", "sk_sketch_round",
+    "sk_ckpt8_quantize", "sk_ckpt8_dequantize", "sk_linear_bwd_lut_ckpt8",
+    "sk_layer_norm_bwd_workspace_bytes", "sk_layer_norm_fwd", "sk_layer_norm_bwd",
+    "sk_cross_entropy_workspace_bytes", "sk_cross_entropy", "sk_scale_bf16",
 )
 
 
@@ -79,6 +86,15 @@ def _load() -> ctypes.CDLL:
         "sk_inverse_factor": ([vp, i64, f64, vp, vp, vp, sz, vp], i32),
         "sk_lloyd": ([vp, vp, i32, i32, i64, i64, i32, vp, vp, vp], i32),
         "sk_sketch_round": ([vp, vp, vp, i32, i32, i64, i64, vp, vp, sz, vp], i32),
+        "sk_ckpt8_quantize": ([vp, i64, i64, vp, vp, vp], i32),
+        "sk_ckpt8_dequantize": ([vp, vp, i64, i64, vp, vp], i32),
+        "sk_linear_bwd_lut_ckpt8": ([vp, i32, i32, i64, i64, vp, vp, vp, i64, vp, i32, vp, i32, vp, sz, vp], i32),
+        "sk_layer_norm_bwd_workspace_bytes": ([i64, i64], sz),
+        "sk_layer_norm_fwd": ([vp, i32, i64, i64, vp, vp, i32, f32, i32, vp, vp, vp, vp, vp, vp], i32),
+        "sk_layer_norm_bwd": ([vp, vp, i32, i64, i64, vp, i32, vp, vp, i32, vp, vp, vp, vp, sz, vp], i32),
+        "sk_cross_entropy_workspace_bytes": ([i64, i64, i64, i32, i32], sz),
+        "sk_cross_entropy": ([vp, vp, vp, i32, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp, sz, vp], i32),
+        "sk_scale_bf16": ([vp, i64, vp, vp], i32),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -388,6 +404,333 @@ def sketch_layer(theta: torch.Tensor, X: torch.Tensor, bits: int, gpr: int, damp
     return pack(idx, bits), lut, idx
 
 
+# ---------------------------------------------------------------------------
+# 8-bit activation checkpoints
+# ---------------------------------------------------------------------------
+
+class Ckpt8(NamedTuple):
+    """An 8-bit checkpoint of bf16 rows [T, d]: int8 q [T, d] and one scale byte
+    per 32 columns, uint8 [T, d // 32] (the format is in sk.h)."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+
+def _on(device: torch.device):
+    """The library works on the current device: make it the tensors' own."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _together(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("every tensor of a call must be on one device")
+
+
+def _need_ckpt8(ck: "Ckpt8"):
+    q, scale = ck
+    _need(q, torch.int8, "q", 2)
+    _need(scale, torch.uint8, "scale", 2)
+    T, d = q.shape
+    if d % 32 or tuple(scale.shape) != (T, d // 32):
+        raise ValueError("scale must hold one byte per 32 columns of q")
+    _together(q, scale)
+    return q, scale, T, d
+
+
+def ckpt8(X: torch.Tensor) -> Ckpt8:
+    """The 8-bit checkpoint of bf16 rows X [T, d] (d a multiple of 32)."""
+    _need(X, torch.bfloat16, "X", 2)
+    T, d = X.shape
+    if d % 32:
+        raise ValueError("d must be a multiple of 32")
+    with _on(X.device):
+        q = torch.empty((T, d), dtype=torch.int8, device=X.device)
+        scale = torch.empty((T, d // 32), dtype=torch.uint8, device=X.device)
+        _check(lib.sk_ckpt8_quantize(_ptr(X), T, d, _ptr(q), _ptr(scale), _stream(X.device)))
+    return Ckpt8(q, scale)
+
+
+def ckpt8_dequant(ck: Ckpt8) -> torch.Tensor:
+    """The bf16 rows [T, d] that a checkpoint stands for."""
+    q, scale, T, d = _need_ckpt8(ck)
+    with _on(q.device):
+        X = torch.empty((T, d), dtype=torch.bfloat16, device=q.device)
+        _check(lib.sk_ckpt8_dequantize(_ptr(q), _ptr(scale), T, d, _ptr(X), _stream(q.device)))
+    return X
+
+
+def linear_bwd_lut_ckpt8(packed: torch.Tensor, bits: int, gpr: int, ck: Ckpt8, dY: torch.Tensor,
+                         task: Optional[torch.Tensor] = None, ntask: int = 1, out: Optional[torch.Tensor] = None,
+                         accumulate: bool = False) -> torch.Tensor:
+    """dlut [ntask, n, gpr, k] fp32 as linear_bwd_lut computes it, for the X that
+    the checkpoint stands for."""
+    q, scale, T, d = _need_ckpt8(ck)
+    _need(dY, torch.bfloat16, "dY", 2)
+    _need(packed, torch.uint8, "packed")
+    n = dY.shape[1]
+    if dY.shape[0] != T:
+        raise ValueError("the checkpoint and dY must have the same number of tokens")
+    if packed.numel() < packed_bytes(n, d, bits):
+        raise ValueError("packed does not hold [n, d] indices")
+    task = _task_arg(task, T)
+    _together(q, dY, packed, task, out)
+    shape = (ntask, n, gpr, 1 << bits)
+    if out is not None:
+        _need(out, torch.float32, "out")
+        if out.numel() != ntask * n * gpr << bits:
+            raise ValueError(f"out must hold {shape} values")
+    elif accumulate:
+        raise ValueError("accumulate adds to out: give it")
+    with _on(q.device):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        ws, nb = _workspace(SK_OP_BWD_LUT_CKPT8, n, d, bits, gpr, T, ntask, q.device)
+        _check(lib.sk_linear_bwd_lut_ckpt8(_ptr(packed), bits, gpr, n, d, _ptr(q), _ptr(scale), _ptr(dY), T, _ptr(task),
+                                           ntask, _ptr(out), int(accumulate), _ptr(ws), nb, _stream(q.device)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Layer norm and RMS norm
+# ---------------------------------------------------------------------------
+
+_NORM_TYPES = {torch.float32: SK_F32, torch.bfloat16: SK_BF16, torch.float16: SK_F16}
+
+
+def _norm_args(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]):
+    if not isinstance(x, torch.Tensor) or x.dtype not in _NORM_TYPES:
+        raise TypeError("x must be a float32, bfloat16 or float16 tensor")
+    _need(x, x.dtype, "x", 2)
+    if weight.dtype not in (x.dtype, torch.float32):
+        raise TypeError("weight must have x's type or float32")
+    _need(weight, weight.dtype, "weight", 1)
+    T, d = x.shape
+    if weight.numel() != d:
+        raise ValueError("weight must hold one value per column")
+    if bias is not None:
+        _need(bias, weight.dtype, "bias", 1)
+        if bias.numel() != d:
+            raise ValueError("bias must hold one value per column")
+    _together(x, weight, bias)
+    return T, d, _NORM_TYPES[x.dtype], _NORM_TYPES[weight.dtype]
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   rms: bool = False, ckpt: bool = False, stats: bool = True):
+    """(y, mean, rstd, checkpoint) of the layer norm (or RMS norm) of x [T, d]:
+    mean and rstd are fp32 [T] for layer_norm_bwd (None without `stats`; mean is
+    None for an RMS norm), the checkpoint is the Ckpt8 of y (None without `ckpt`)."""
+    T, d, xt, wt = _norm_args(x, weight, bias)
+    if ckpt and (x.dtype != torch.bfloat16 or d % 32):
+        raise ValueError("a checkpoint needs bf16 rows whose length is a multiple of 32")
+    dev = x.device
+    with _on(dev):
+        y = torch.empty_like(x)
+        mean = torch.empty(T, dtype=torch.float32, device=dev) if stats and not rms else None
+        rstd = torch.empty(T, dtype=torch.float32, device=dev) if stats else None
+        ck = None
+        if ckpt:
+            ck = Ckpt8(torch.empty((T, d), dtype=torch.int8, device=dev),
+                       torch.empty((T, d // 32), dtype=torch.uint8, device=dev))
+        _check(lib.sk_layer_norm_fwd(_ptr(x), xt, T, d, _ptr(weight), _ptr(bias), wt, eps, int(rms), _ptr(y), _ptr(mean),
+                                     _ptr(rstd), _ptr(ck.q) if ck else None, _ptr(ck.scale) if ck else None,
+                                     _stream(dev)))
+    return y, mean, rstd, ck
+
+
+def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: Optional[torch.Tensor],
+                   rstd: torch.Tensor, rms: bool = False, bias: bool = True, need_dx: bool = True,
+                   need_dw: bool = True):
+    """(dx, dw, db) of layer_norm_fwd (None where not wanted): dx has x's type, dw
+    and db the weight's."""
+    T, d, xt, wt = _norm_args(x, weight, None)
+    _need(dy, x.dtype, "dy", 2)
+    if dy.shape != x.shape:
+        raise ValueError("dy must have x's shape")
+    for t, name in ((rstd, "rstd"), (None if rms else mean, "mean")):
+        if t is None and rms and name == "mean":
+            continue
+        _need(t, torch.float32, name, 1)
+        if t.numel() != T:
+            raise ValueError(f"{name} must hold one value per row")
+    _together(x, dy, rstd, None if rms else mean)
+    dev = x.device
+    with _on(dev):
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty_like(weight) if need_dw else None
+        db = torch.empty_like(weight) if bias else None
+        ws, nb = None, 0
+        if need_dw or bias:
+            nb = int(lib.sk_layer_norm_bwd_workspace_bytes(T, d))
+            ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+        _check(lib.sk_layer_norm_bwd(_ptr(dy), _ptr(x), xt, T, d, _ptr(weight), wt, None if rms else _ptr(mean),
+                                     _ptr(rstd), int(rms), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nb, _stream(dev)))
+    return dx, dw, db
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """layer_norm_fwd / layer_norm_bwd as an autograd function of x, weight and bias."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, rms, ckpt):
+        y, mean, rstd, ck = layer_norm_fwd(x, weight, bias, eps, rms, ckpt)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.rms = rms
+        if ck is None:
+            return y
+        ctx.mark_non_differentiable(ck.q, ck.scale)
+        return y, ck.q, ck.scale
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, *_):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = layer_norm_bwd(dy.to(x.dtype).contiguous(), x, weight, mean, rstd, ctx.rms, need[2], need[0],
+                                    need[1])
+        return dx, dw, db, None, None, None
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               rms: bool = False, ckpt: bool = False):
+    """Layer norm (RMS norm with `rms`) over the last dimension of x [..., d], an
+    autograd function of x, weight and bias.  With `ckpt` it returns (y, Ckpt8 of
+    y's rows) for a SketchedLinear that keeps its input in 8 bits."""
+    lead = x.shape[:-1]
+    rows = x.reshape(-1, x.shape[-1]).contiguous()
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))):
+        y, _, _, ck = layer_norm_fwd(rows, weight, bias, eps, rms, ckpt, stats=False)
+        y = y.reshape(*lead, x.shape[-1])
+        return (y, ck) if ckpt else y
+    out = LayerNormFunction.apply(rows, weight, bias, eps, rms, ckpt)
+    if not ckpt:
+        return out.reshape(*lead, x.shape[-1])
+    return out[0].reshape(*lead, x.shape[-1]), Ckpt8(out[1], out[2])
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer norm (RMS norm with `rms`, then without a bias unless asked for) of
+    [..., d] activations; forward(x, ckpt) as layer_norm."""
+
+    def __init__(self, d: int, eps: float = 1e-5, rms: bool = False, bias: Optional[bool] = None,
+                 dtype: torch.dtype = torch.float32, device=None):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.ones(d, dtype=dtype, device=device))
+        self.bias = (torch.nn.Parameter(torch.zeros(d, dtype=dtype, device=device))
+                     if (not rms if bias is None else bias) else None)
+        self.eps = eps
+        self.rms = rms
+
+    def forward(self, x: torch.Tensor, ckpt: bool = False):
+        return layer_norm(x, self.weight, self.bias, self.eps, self.rms, ckpt)
+
+
+# ---------------------------------------------------------------------------
+# Linear cross entropy: the head product and its loss
+# ---------------------------------------------------------------------------
+
+_REDUCTIONS = {"none": SK_CE_NONE, "mean": SK_CE_MEAN, "sum": SK_CE_SUM}
+
+
+def cross_entropy(H: torch.Tensor, W: torch.Tensor, target: torch.Tensor, ignore_index: int = -100,
+                  reduction: str = "mean", dloss: Optional[torch.Tensor] = None, need_loss: bool = True,
+                  need_dh: bool = False, need_dw: bool = False):
+    """(loss, dH, dW) of the softmax cross entropy of H W^T against target, None
+    where not wanted.  H bf16 [T, d], W bf16 [V, d], target int32 or int64 [T];
+    loss fp32, [T] for reduction "none", else a scalar; dloss: the loss's own
+    gradient (fp32, its shape), ones when None."""
+    _need(H, torch.bfloat16, "H", 2)
+    _need(W, torch.bfloat16, "W", 2)
+    if not isinstance(target, torch.Tensor) or target.dtype not in (torch.int32, torch.int64):
+        raise TypeError("target must be an int32 or int64 tensor")
+    _need(target, target.dtype, "target", 1)
+    T, d = H.shape
+    V = W.shape[0]
+    if W.shape[1] != d:
+        raise ValueError("H and W must have the same number of columns")
+    if target.numel() != T:
+        raise ValueError("target must hold one class per token")
+    if reduction not in _REDUCTIONS:
+        raise ValueError('reduction must be "none", "mean" or "sum"')
+    red = _REDUCTIONS[reduction]
+    if dloss is not None:
+        _need(dloss, torch.float32, "dloss")
+        if dloss.numel() != (T if red == SK_CE_NONE else 1):
+            raise ValueError("dloss must have the loss's shape")
+    _together(H, W, target, dloss)
+    dev = H.device
+    with _on(dev):
+        loss = torch.empty((T,) if red == SK_CE_NONE else (), dtype=torch.float32, device=dev) if need_loss else None
+        dH = torch.empty_like(H) if need_dh else None
+        dW = torch.empty_like(W) if need_dw else None
+        nb = int(lib.sk_cross_entropy_workspace_bytes(T, V, d, int(need_dh), int(need_dw)))
+        ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+        _check(lib.sk_cross_entropy(_ptr(H), _ptr(W), _ptr(target), target.element_size() * 8, T, V, d, ignore_index,
+                                    red, _ptr(dloss), _ptr(loss), _ptr(dH), _ptr(dW), _ptr(ws), nb, _stream(dev)))
+    return loss, dH, dW
+
+
+class LinearCrossEntropyFunction(torch.autograd.Function):
+    """cross_entropy as an autograd function of H and W.
+
+    A reduced loss's gradient is known up to one factor, so the forward pass
+    computes loss and gradients together (the logits' product is not repeated)
+    and the backward pass scales them in place by the incoming gradient, which a
+    factor of 1 leaves alone.  They are handed out once; a second backward pass
+    over a retained graph computes them again, as does reduction "none", whose
+    gradient needs every token's factor."""
+
+    @staticmethod
+    def forward(ctx, H, W, target, ignore_index, reduction):
+        dh, dw = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        now = reduction != "none"
+        loss, dH, dW = cross_entropy(H, W, target, ignore_index, reduction, need_dh=dh and now, need_dw=dw and now)
+        ctx.save_for_backward(H, W, target)
+        ctx.args = (ignore_index, reduction)
+        ctx.ready = (dH, dW) if now else None
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        H, W, target = ctx.saved_tensors
+        dh, dw = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        g = g.to(torch.float32).contiguous()
+        if ctx.ready is None:
+            _, dH, dW = cross_entropy(H, W, target, *ctx.args, dloss=g, need_loss=False, need_dh=dh, need_dw=dw)
+            return dH, dW, None, None, None
+        dH, dW = ctx.ready
+        ctx.ready = None
+        with _on(H.device):
+            for t in (dH, dW):
+                if t is not None:
+                    _check(lib.sk_scale_bf16(_ptr(t), t.numel(), _ptr(g), _stream(H.device)))
+        return dH, dW, None, None, None
+
+
+def linear_cross_entropy(H: torch.Tensor, W: torch.Tensor, target: torch.Tensor, ignore_index: int = -100,
+                         reduction: str = "mean") -> torch.Tensor:
+    """Softmax cross entropy of the logits H W^T (H bf16 [..., d], W bf16 [V, d])
+    against target [...], an autograd function of H and W that never holds the
+    logits.  Tokens whose target is ignore_index take no part; "mean" divides by
+    the others' number (0 when there are none)."""
+    lead = H.shape[:-1]
+    if target.shape != lead:
+        raise ValueError("target must hold one class per token")
+    args = (H.reshape(-1, H.shape[-1]).contiguous(), W.contiguous(), target.reshape(-1).contiguous())
+    if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
+        loss = LinearCrossEntropyFunction.apply(*args, ignore_index, reduction)
+    else:
+        loss = cross_entropy(*args, ignore_index, reduction)[0]
+    return loss.reshape(lead) if reduction == "none" else loss
+
+
+# ---------------------------------------------------------------------------
+# The layer as an autograd function and a module
+# ---------------------------------------------------------------------------
+
 class SketchedLinearFunction(torch.autograd.Function):
     """Y = X Theta_hat^T with gradients for X and for the LUT values only.
 
@@ -422,15 +765,56 @@ class SketchedLinearFunction(torch.autograd.Function):
         return dX, dlut, None, None, None, None
 
 
+class SketchedLinearCkpt8Function(torch.autograd.Function):
+    """SketchedLinearFunction that keeps X as an 8-bit checkpoint (q, scale) for
+    the LUT gradient.  The forward product uses X itself, and the gradient for X
+    does not need X, so only the LUT gradient sees the rounding to 8 bits."""
+
+    @staticmethod
+    def forward(ctx, X, lut, lut16, packed, bits, task, q, scale):
+        Y = linear_fwd(packed, lut16, bits, X, task)
+        if ctx.needs_input_grad[1]:
+            if q is None:
+                q, scale = ckpt8(X)
+        else:
+            q = scale = None
+        ctx.save_for_backward(lut16, packed, task, q, scale)
+        ctx.bits = bits
+        ctx.in_features = X.shape[1]
+        ctx.lut_dtype = lut.dtype
+        return Y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        lut16, packed, task, q, scale = ctx.saved_tensors
+        dY = dY.to(torch.bfloat16).contiguous()
+        ntask, n, gpr, _ = lut16.shape
+        dX = dlut = None
+        if ctx.needs_input_grad[0]:
+            dX = linear_bwd_input(packed, lut16, ctx.bits, ctx.in_features, dY, task)
+        if ctx.needs_input_grad[1]:
+            dlut = linear_bwd_lut_ckpt8(packed, ctx.bits, gpr, Ckpt8(q, scale), dY, task, ntask).to(ctx.lut_dtype)
+        return dX, dlut, None, None, None, None, None, None
+
+
 def sketched_linear(X: torch.Tensor, lut: torch.Tensor, packed: torch.Tensor, bits: int,
-                    task: Optional[torch.Tensor] = None, lut16: Optional[torch.Tensor] = None) -> torch.Tensor:
+                    task: Optional[torch.Tensor] = None, lut16: Optional[torch.Tensor] = None,
+                    ckpt=False) -> torch.Tensor:
     """Y = X Theta_hat^T as an autograd function of X and of the LUT values.
 
     lut: fp32 master LUTs (their gradient stays fp32) or fp16 LUTs (their
     gradient is rounded to fp16).  lut16: the fp16 tables of an fp32 master,
-    when the caller keeps them (else they are rounded from `lut` here)."""
+    when the caller keeps them (else they are rounded from `lut` here).
+    ckpt: keep X in 8 bits for the LUT gradient, either a Ckpt8 of X that the
+    caller has (layers that share an input share it) or True to make one here."""
     if lut16 is None:
         lut16 = lut if lut.dtype == torch.float16 else lut.detach().to(torch.float16)
+    if ckpt is not False and ckpt is not None:
+        q, scale = (None, None) if ckpt is True else ckpt
+        if q is not None and tuple(q.shape) != tuple(X.shape):
+            raise ValueError("the checkpoint must have X's shape")
+        return SketchedLinearCkpt8Function.apply(X.contiguous(), lut, lut16, packed, bits, task, q, scale)
     return SketchedLinearFunction.apply(X, lut, lut16, packed, bits, task)
 
 
@@ -446,10 +830,15 @@ class SketchedLinear(torch.nn.Module):
     `lut16` follows the master: `adamw_step` / `sgd_step` update both in one
     library call; any other in-place change of `lut` (a torch optimizer) is
     noticed by its version counter and `lut16` is rounded again before the
-    next forward."""
+    next forward.
 
-    def __init__(self, packed: torch.Tensor, lut: torch.Tensor, bits: int, in_features: int):
+    ckpt8=True keeps the layer's input in 8 bits instead of bf16 between the
+    forward and the backward pass; forward(X, task, ckpt) then takes the Ckpt8 of
+    X from a caller that has one (layer_norm(..., ckpt=True)) or makes its own."""
+
+    def __init__(self, packed: torch.Tensor, lut: torch.Tensor, bits: int, in_features: int, ckpt8: bool = False):
         super().__init__()
+        self.ckpt8 = ckpt8
         self.register_buffer("packed", packed)
         self.lut = torch.nn.Parameter(lut.detach().to(torch.float32).contiguous())
         self.register_buffer("lut16", lut.detach().to(torch.float16).contiguous())
@@ -469,17 +858,17 @@ class SketchedLinear(torch.nn.Module):
 
     @classmethod
     def from_dense(cls, weight: torch.Tensor, X_calib: torch.Tensor, bits: int, gpr: int, ntask: int = 1,
-                   damp: float = 0.01, max_iter: int = 100) -> "SketchedLinear":
+                   damp: float = 0.01, max_iter: int = 100, ckpt8: bool = False) -> "SketchedLinear":
         """Sketch a dense weight [n, d] with calibration activations [s, d]
         (bf16); every LUT set starts from the same learned centroids."""
         packed, lut, _ = sketch_layer(weight.float().contiguous(), X_calib, bits, gpr, damp, max_iter)
-        return cls(packed, lut.unsqueeze(0).repeat(ntask, 1, 1, 1).contiguous(), bits, weight.shape[1])
+        return cls(packed, lut.unsqueeze(0).repeat(ntask, 1, 1, 1).contiguous(), bits, weight.shape[1], ckpt8)
 
-    def forward(self, X: torch.Tensor, task: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def forward(self, X: torch.Tensor, task: Optional[torch.Tensor] = None, ckpt: Optional[Ckpt8] = None) -> torch.Tensor:
         self._sync_lut16()
         lead = X.shape[:-1]
         Y = sketched_linear(X.reshape(-1, self.in_features).to(torch.bfloat16).contiguous(), self.lut, self.packed,
-                            self.bits, task, lut16=self.lut16)
+                            self.bits, task, lut16=self.lut16, ckpt=ckpt if ckpt is not None else self.ckpt8)
         return Y.reshape(*lead, self.out_features)
 
     def adamw_step(self, m: torch.Tensor, v: torch.Tensor, step: int, lr: float, beta1: float = 0.9,

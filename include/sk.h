@@ -88,11 +88,24 @@ typedef enum {
                                     Gram matrix is not positive definite       */
 #define SK_CHECK_LUT_ORDER 16u   /* sk_sketch_round was given a LUT that is not
                                     ascending                                   */
+#define SK_CHECK_TARGET_RANGE 32u /* sk_cross_entropy saw a class outside [0, V)
+                                    that is not ignore_index                    */
 
 /* Operation selectors for sk_workspace_bytes. */
 #define SK_OP_FWD 0
 #define SK_OP_BWD_INPUT 1
 #define SK_OP_BWD_LUT 2
+#define SK_OP_BWD_LUT_CKPT8 3
+
+/* Element types of the norm calls. */
+#define SK_F32 0
+#define SK_BF16 1
+#define SK_F16 2
+
+/* Reductions of sk_cross_entropy. */
+#define SK_CE_NONE 0
+#define SK_CE_MEAN 1
+#define SK_CE_SUM 2
 
 int sk_abi_version(void);
 const char* sk_status_string(sk_status s);
@@ -248,6 +261,93 @@ sk_status sk_linear_bwd_lut_noalloc(const void* packed, int bits, int gpr, int64
                                     const uint16_t* X, const uint16_t* dY, int64_t T,
                                     const int32_t* task, int ntask, float* dlut, int accumulate,
                                     sk_stream_t stream);
+
+/*
+ * 8-bit activation checkpoints.  The LUT gradient needs the layer's input X
+ * after the whole forward pass has run; kept as a checkpoint it costs 33/32
+ * bytes per value instead of 2.
+ *
+ * Format: a row of d values (d % 32 == 0) in blocks of 32 columns.  A block has
+ * an exponent e, the least integer with max|x| <= 127 * 2^e, kept in
+ * [-126, 121], and 32 int8 values q = x * 2^-e rounded to nearest, ties to even
+ * (|q| <= 127).  It stands for q * 2^e, which is exact in bf16 and at most
+ * 2^(e-1) from x.  q is [T][d]; scale is [T][d / 32] bytes e + 127.  A block that
+ * holds a NaN or an infinity gets the byte 255 and reads back as NaNs.
+ *
+ * sk_ckpt8_quantize: X (bf16 [T][d]) -> q, scale.
+ * sk_ckpt8_dequantize: q, scale -> X (bf16 [T][d]), the values the block stands for.
+ *
+ * sk_linear_bwd_lut_ckpt8: sk_linear_bwd_lut with X given as a checkpoint: the
+ * gradient for the values that it stands for, without a bf16 copy of X.  Shape
+ * rules, task rules and errors are those of sk_linear_bwd_lut; the workspace is
+ * sk_workspace_bytes(SK_OP_BWD_LUT_CKPT8, ...) bytes when that is not 0 and is
+ * required then.  Deterministic, with several LUT sets too.
+ */
+sk_status sk_ckpt8_quantize(const uint16_t* X, int64_t T, int64_t d, int8_t* q, uint8_t* scale, sk_stream_t stream);
+sk_status sk_ckpt8_dequantize(const int8_t* q, const uint8_t* scale, int64_t T, int64_t d, uint16_t* X,
+                              sk_stream_t stream);
+sk_status sk_linear_bwd_lut_ckpt8(const void* packed, int bits, int gpr, int64_t n, int64_t d, const int8_t* q,
+                                  const uint8_t* scale, const uint16_t* dY, int64_t T, const int32_t* task, int ntask,
+                                  float* dlut, int accumulate, void* workspace, size_t workspace_bytes,
+                                  sk_stream_t stream);
+
+/*
+ * Layer norm (rms == 0) and RMS norm (rms == 1, no mean taken off) of T rows of
+ * d values, 1 <= d <= 32768:
+ *   xh = (x - mean) * rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps),
+ *   y = xh * w + b.
+ * x, y, dy and dx have the type xtype (SK_F32, SK_BF16, SK_F16); w, b, dw and db
+ * have wtype, which is xtype or SK_F32.  fp32 arithmetic, each output rounded
+ * once.  b may be NULL.  eps >= 0.
+ *
+ * sk_layer_norm_fwd: mean and rstd (fp32 [T]) receive the row statistics for the
+ * backward pass; either may be NULL (mean is written as 0 by an RMS norm).  q and
+ * scale, both or neither: the 8-bit checkpoint of y as rounded (xtype SK_BF16,
+ * d % 32 == 0).
+ *
+ * sk_layer_norm_bwd: dx, dw, db from dy (each may be NULL when it is not wanted;
+ * mean may be NULL for an RMS norm).  dw = sum over rows of dy * xh and
+ * db = sum over rows of dy, summed in fp32 in a fixed order (deterministic).
+ * workspace: sk_layer_norm_bwd_workspace_bytes(T, d) bytes when dw or db is wanted.
+ * T == 0 writes zeros to dw and db.
+ */
+size_t sk_layer_norm_bwd_workspace_bytes(int64_t T, int64_t d);
+sk_status sk_layer_norm_fwd(const void* x, int xtype, int64_t T, int64_t d, const void* w, const void* b, int wtype,
+                            float eps, int rms, void* y, float* mean, float* rstd, int8_t* q, uint8_t* scale,
+                            sk_stream_t stream);
+sk_status sk_layer_norm_bwd(const void* dy, const void* x, int xtype, int64_t T, int64_t d, const void* w, int wtype,
+                            const float* mean, const float* rstd, int rms, void* dx, void* dw, void* db,
+                            void* workspace, size_t workspace_bytes, sk_stream_t stream);
+
+/*
+ * sk_cross_entropy: the head product, softmax cross entropy over the vocabulary
+ * and its gradients, without a [T][V] tensor of logits:
+ *   l = H W^T (bf16 H [T][d], W [V][d], fp32 accumulation),
+ *   loss[t] = log(sum_v exp(l[t][v])) - l[t][target[t]].
+ * target: class ids, int32 (target_bits 32) or int64 (64), device [T].  A token
+ * whose id is ignore_index takes no part: its loss is 0 and its gradient is
+ * zero.  Any other id outside [0, V) sets SK_CHECK_TARGET_RANGE and is treated the
+ * same way.
+ * reduction: SK_CE_NONE (loss is fp32 [T]), SK_CE_MEAN (fp32 [1], the mean over the
+ * tokens that take part, 0 if there are none) or SK_CE_SUM (fp32 [1]).  loss may be
+ * NULL when only gradients are wanted.
+ * dH (bf16 [T][d]) and dW (bf16 [V][d]): the gradients, each NULL when it is not
+ * wanted.  dloss: the gradient of the result, fp32 on the device, [T] with
+ * SK_CE_NONE and [1] otherwise; NULL means ones.  Probabilities are rounded to
+ * bf16 for the two gradient products, sums are fp32.
+ * 1 <= V < 2^24, 8 <= d < 2^20, d % 8 == 0.  T == 0: a reduced loss is 0, dW is
+ * zeroed.  workspace: sk_cross_entropy_workspace_bytes(T, V, d, dH != NULL,
+ * dW != NULL) bytes; with gradients it holds one chunk of tokens' exponentials
+ * (512 MiB at most, or 256 tokens' if that is more).  Deterministic.
+ *
+ * sk_scale_bf16: x (bf16 [count], count % 8 == 0) times the device scalar *factor,
+ * in place; a factor of exactly 1 leaves x alone.
+ */
+size_t sk_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t d, int want_dh, int want_dw);
+sk_status sk_cross_entropy(const uint16_t* H, const uint16_t* W, const void* target, int target_bits, int64_t T,
+                           int64_t V, int64_t d, int64_t ignore_index, int reduction, const float* dloss, float* loss,
+                           uint16_t* dH, uint16_t* dW, void* workspace, size_t workspace_bytes, sk_stream_t stream);
+sk_status sk_scale_bf16(uint16_t* x, int64_t count, const float* factor, sk_stream_t stream);
 
 /*
  * sk_bin_counts: the static bin sizes of the one-hot sketch (Eq. 1),

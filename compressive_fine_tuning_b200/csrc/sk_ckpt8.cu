@@ -9,14 +9,22 @@ namespace sk {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnits = 4;      // 16-byte loads in flight per thread
 
 __global__ void __launch_bounds__(kThreads) ckpt8_quantize_kernel(const uint4* __restrict__ X, int64_t units,
                                                                   uint2* __restrict__ q, uint8_t* __restrict__ scale) {
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  // whole warps stay in the loop together: the shuffles name every lane
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u - (threadIdx.x & 31) < units; u += step) {
-    const uint4 v = u < units ? X[u] : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  // whole warps run through the shuffles: units beyond the end are zeros
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+  uint4 v[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = first + i * kThreads;
+    v[i] = u < units ? X[u] : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = first + i * kThreads;
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     uint32_t byte;
     const uint2 o = ckpt8_quantize8(w, byte);
     if (u < units) {
@@ -29,22 +37,31 @@ __global__ void __launch_bounds__(kThreads) ckpt8_quantize_kernel(const uint4* _
 __global__ void __launch_bounds__(kThreads) ckpt8_dequantize_kernel(const uint2* __restrict__ q,
                                                                     const uint8_t* __restrict__ scale, int64_t units,
                                                                     uint4* __restrict__ X) {
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += step) {
-    const uint2 v = q[u];
-    const float s = __uint_as_float((uint32_t)scale[u >> 2] << 23);
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+  uint2 v[kUnits];
+  uint32_t byte[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = first + i * kThreads;
+    if (u < units) {
+      v[i] = q[u];
+      byte[i] = scale[u >> 2];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int64_t u = first + i * kThreads;
+    if (u >= units) break;
     uint4 o;
-    ckpt8_dequant4(v.x, s, o.x, o.y);
-    ckpt8_dequant4(v.y, s, o.z, o.w);
+    const uint32_t s2 = ckpt8_scale2(byte[i]);
+    ckpt8_dequant4(v[i].x, s2, o.x, o.y);
+    ckpt8_dequant4(v[i].y, s2, o.z, o.w);
     X[u] = o;
   }
 }
 
-unsigned grid_for(int64_t units) {
-  const int64_t blocks = (units + kThreads - 1) / kThreads;
-  const int64_t cap = (int64_t)1 << 30;
-  return (unsigned)(blocks < cap ? blocks : cap);
-}
+// T * d < 2^62 / 8 units, 1024 per block: the grid's x extent reaches 2^31 blocks
+unsigned grid_for(int64_t units) { return (unsigned)((units + kThreads * kUnits - 1) / (kThreads * kUnits)); }
 
 }  // namespace
 

@@ -55,17 +55,31 @@ __device__ __forceinline__ uint2 ckpt8_quantize8(const uint32_t (&w)[4], uint32_
   return make_uint2(four(b[0], b[1], b[2], b[3]), four(b[4], b[5], b[6], b[7]));
 }
 
-// Four int8 values times 2^e (scale = the fp32 with the block's byte as its
-// exponent field) as two bf16x2 words.  Exact: the upper halves of the fp32
-// products hold all of their bits.
-__device__ __forceinline__ void ckpt8_dequant4(uint32_t q4, float scale, uint32_t& w0, uint32_t& w1) {
-  const uint32_t u = q4 ^ 0x80808080u;                              // q + 128
-  float f[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f[i] = (__uint_as_float(prmt(u, 0x4b000000u, 0x7540u + i)) - 8388736.f) * scale;   // 2^23 + u
-  w0 = prmt(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x7632);
-  w1 = prmt(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x7632);
+// Two int8 values in the low bytes of the halves of `t` -> bf16x2 of the two,
+// exactly: 128 + (the low seven bits) has an ulp of one, and what comes off it is
+// 128, or 256 for a negative value -- the sign bit sits where those two constants
+// differ (the lowest exponent bit), so one logic operation forms each term.
+__device__ __forceinline__ uint32_t int8x2_to_bf16x2(uint32_t t) {
+  const uint32_t m = (t & 0x007f007fu) | 0x43004300u;
+  const uint32_t c = (t & 0x00800080u) | 0xc300c300u;
+  const __nv_bfloat162 v = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// bf16x2 of a block's scale 2^e from its byte (255 gives infinity)
+__device__ __forceinline__ uint32_t ckpt8_scale2(uint32_t byte) { return (byte << 7) | (byte << 23); }
+
+// Four int8 values times 2^e as two bf16x2 words, exactly (q has at most seven
+// significant bits; 0 * inf is the NaN of a block that was not finite).
+__device__ __forceinline__ void ckpt8_dequant4(uint32_t q4, uint32_t scale2, uint32_t& w0, uint32_t& w1) {
+  const uint32_t t = prmt(q4, 0u, 0x3120);                          // bytes 0 2 1 3
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&scale2);
+  uint32_t a = int8x2_to_bf16x2(t), b = int8x2_to_bf16x2(t >> 8);
+  const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), s);
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), s);
+  w0 = *reinterpret_cast<const uint32_t*>(&x);
+  w1 = *reinterpret_cast<const uint32_t*>(&y);
 }
 
 // launchers

@@ -29,17 +29,50 @@ static_assert(SMEM <= 232448, "one CTA's shared memory");
 
 struct Shape {
   int mt, nt, ksteps;    // tiles and K steps
+  int tn;                // columns per tile: 256, or less for a K-major B (a multiple of 32)
   int group;             // M tiles walked together (see tile_at)
+  // The last wave: the `split_from`-th and later tiles are cut along K into `split`
+  // parts, one per pair, so that a few left-over tiles do not keep one pair each
+  // busy for a whole tile while the others idle.  A part's accumulator goes to the
+  // epilogue with its index; the caller joins the parts.
+  int split_from, split;
 };
+
+struct Item {
+  int m, n, k0, k1;
+  int part;              // -1: a whole tile
+};
+
+__host__ __device__ inline int items(const Shape& s) {
+  return s.split_from + (s.mt * s.nt - s.split_from) * s.split;
+}
 
 // Tiles in bands of `group` M tiles, N outside and M inside a band: the pairs in
 // flight share a few B tiles and one band of A.
-__device__ __forceinline__ void tile_at(const Shape& s, int i, int& m, int& n) {
+__host__ __device__ inline void tile_at(const Shape& s, int i, int& m, int& n) {
   const int per = s.group * s.nt;
   const int band = i / per, r = i - band * per;
-  const int rows = min(s.group, s.mt - band * s.group);
+  const int left = s.mt - band * s.group;
+  const int rows = left < s.group ? left : s.group;
   n = r / rows;
   m = band * s.group + (r - n * rows);
+}
+
+__device__ __forceinline__ Item item_at(const Shape& s, int i) {
+  Item it;
+  it.k0 = 0;
+  it.k1 = s.ksteps;
+  it.part = -1;
+  int tile = i;
+  if (i >= s.split_from && s.split > 1) {
+    it.part = i - s.split_from;
+    const int q = it.part % s.split;
+    tile = s.split_from + it.part / s.split;
+    it.k0 = (int)((int64_t)s.ksteps * q / s.split);
+    it.k1 = (int)((int64_t)s.ksteps * (q + 1) / s.split);
+  }
+  tile_at(s, tile, it.m, it.n);
+  return it;
 }
 
 // Output rows staged by one warp: 32 rows x 64 16-bit values in the 128-byte
@@ -73,13 +106,14 @@ struct SlabWriter {
 };
 
 // Epi: struct with
-//   void tile(uint32_t tmem, int m0, int n0, int warp, int lane, SlabWriter&)
-// called by every epilogue warp for every tile: the warp's accumulator rows are
-// m0 + 32 warp + lane (TMEM lanes), columns n0 .. n0 + 255.
+//   void tile(uint32_t tmem, int m0, int n0, int part, int warp, int lane, SlabWriter&)
+// called by every epilogue warp for every item: the warp's accumulator rows are
+// m0 + 32 warp + lane (TMEM lanes), columns n0 .. n0 + tn - 1.
 template <int A_MN, int B_MN, class Epi>
 __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* tm_b, const Shape& sh, Epi& epi,
                                     unsigned int* check) {
-  constexpr uint32_t IDESC = tc::idesc_bf16(TM, TN, A_MN, B_MN);
+  const uint32_t idesc = tc::idesc_bf16(TM, B_MN ? TN : sh.tn, A_MN, B_MN);
+  const int tn = B_MN ? TN : sh.tn, half_n = tn / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + BAR_OFF);   // even CTA: both CTAs' operands landed
@@ -92,7 +126,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
   const int warp = tc::warp_id(), lane = tc::lane_id();
   const int rank = (int)tc::cluster_ctarank();                     // 0: issues the MMAs
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tiles = sh.mt * sh.nt;
+  const int count = items(sh);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -120,16 +154,16 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
   if (warp == TMA_WARP) {
     if (lane == 0) {
       int it = 0;
-      for (int i = pair; i < tiles && !*abort_flag; i += pairs) {
-        int m, n;
-        tile_at(sh, i, m, n);
-        const int m0 = m * TM + 128 * rank, n0 = n * TN + 128 * rank;
-        for (int k = 0; k < sh.ksteps; ++k, ++it) {
+      const uint32_t bytes = 2u * (A_BYTES + half_n * KS * 2);             // both CTAs' operands of a step
+      for (int i = pair; i < count && !*abort_flag; i += pairs) {
+        const Item w = item_at(sh, i);
+        const int m0 = w.m * TM + 128 * rank, n0 = w.n * tn + half_n * rank;
+        for (int k = w.k0; k < w.k1; ++k, ++it) {
           const int s = it % S;
           if (*abort_flag || !tc::mbar_wait(&empty[s], ((it / S) & 1) ^ 1, check)) { *abort_flag = 1; break; }
           uint8_t* a = smem + s * STAGE;
           uint8_t* b = a + A_BYTES;
-          if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * STAGE);   // the bytes of both CTAs
+          if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], bytes);
           const uint32_t bar = tc::mapa(&full[s], 0);
           if (A_MN) {
             tc::tma_load_2d_pair(a, tm_a, bar, m0, k * KS);
@@ -154,12 +188,13 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
     if (rank == 0 && lane == 0) {
       int it = 0, j = 0;
       bool ok = true;
-      for (int i = pair; i < tiles && ok; i += pairs, ++j) {
+      for (int i = pair; i < count && ok; i += pairs, ++j) {
+        const Item w = item_at(sh, i);
         const int b = j & 1;
         if (*abort_flag || !tc::mbar_wait(&acc_empty[b], ((j >> 1) & 1) ^ 1, check)) { *abort_flag = 1; break; }
         tc::tc_fence_after();
         const uint32_t acc = tc::tmem_addr(tmem, 0, b * TN);
-        for (int k = 0; k < sh.ksteps; ++k, ++it) {
+        for (int k = w.k0; k < w.k1; ++k, ++it) {
           const int s = it % S;
           if (*abort_flag || !tc::mbar_wait(&full[s], (it / S) & 1, check)) { *abort_flag = 1; ok = false; break; }
           tc::tc_fence_after();
@@ -170,7 +205,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
                                      : tc::sdesc(ab + kk * 32, 16, 1024, tc::kSwizzle128);
             const uint64_t bd = B_MN ? tc::sdesc(bb + kk * 2048, 8192, 1024, tc::kSwizzle128)
                                      : tc::sdesc(bb + kk * 32, 16, 1024, tc::kSwizzle128);
-            tc::mma_ss_pair(acc, ad, bd, IDESC, (k > 0 || kk > 0) ? 1u : 0u);
+            tc::mma_ss_pair(acc, ad, bd, idesc, (k > w.k0 || kk > 0) ? 1u : 0u);
           }
           tc::mma_commit_pair(&empty[s]);
         }
@@ -181,15 +216,14 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
     SlabWriter out{smem + SLAB_OFF + warp * 2 * SLAB, 0};
     const uint32_t acc_empty_even = tc::mapa(&acc_empty[0], 0);
     int j = 0;
-    for (int i = pair; i < tiles; i += pairs, ++j) {
+    for (int i = pair; i < count; i += pairs, ++j) {
       const int b = j & 1;
       bool have = !*abort_flag && tc::mbar_wait(&acc_full[b], (j >> 1) & 1, check);
       have = __all_sync(0xffffffffu, have);   // tcgen05.ld is warp-collective
       if (!have) { *abort_flag = 1; break; }
       tc::tc_fence_after();
-      int m, n;
-      tile_at(sh, i, m, n);
-      epi.tile(tc::tmem_addr(tmem, 32 * warp, b * TN), m * TM + 128 * rank, n * TN, warp, lane, out);
+      const Item w = item_at(sh, i);
+      epi.tile(tc::tmem_addr(tmem, 32 * warp, b * TN), w.m * TM + 128 * rank, w.n * tn, w.part, warp, lane, out);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_cluster(acc_empty_even + 8 * b);

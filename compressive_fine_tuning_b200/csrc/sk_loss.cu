@@ -35,6 +35,7 @@ namespace {
 
 constexpr int64_t kExpBytes = int64_t(512) << 20;   // buffer of one chunk's exponentials
 constexpr int64_t kLossChunk = 32768;               // tokens per launch when only the loss is wanted
+constexpr int kMinTile = 128;                       // fewest classes per tile of a loss without gradients
 constexpr float kLog2e = 1.4426950408889634f;
 
 __host__ __device__ constexpr int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
@@ -70,13 +71,14 @@ struct LogitEpi {
   const void* target;
   int target64;
   int64_t ignore_index;
-  int T, V;                 // tokens of the chunk
+  int T, V, tn;             // tokens of the chunk, classes, classes per tile
   bool store;
   unsigned int* check;
 
-  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, int warp, int lane, gemm::SlabWriter& out) {
+  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, int, int warp, int lane, gemm::SlabWriter& out) {
     const int t = m0 + 32 * warp + lane;
-    const int cols = min(gemm::TN, V - n0);
+    if (m0 + 32 * warp >= T) return;
+    const int cols = min(tn, V - n0);
     int64_t y = -1;
     if (t < T) y = class_of(target, target64, t, V, ignore_index, check);
     const int rel = y >= n0 && y < n0 + cols ? (int)(y - n0) : -1;
@@ -129,9 +131,9 @@ struct LogitEpi {
         }
         sum += part;
       }
-      if (store && m0 + 32 * warp < T) out.put(tm_e, e, n0 + 64 * h, m0 + 32 * warp, lane);
+      if (store) out.put(tm_e, e, n0 + 64 * h, m0 + 32 * warp, lane);
     }
-    if (t < T) stats[(int64_t)(n0 / gemm::TN) * T + t] = make_float2(m, sum);
+    if (t < T) stats[(int64_t)(n0 / tn) * T + t] = make_float2(m, sum);
   }
 };
 
@@ -149,7 +151,8 @@ struct LogitArgs {
 __global__ void __launch_bounds__(gemm::THREADS, 1)
 logit_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_w,
              const __grid_constant__ CUtensorMap tm_e, LogitArgs a) {
-  LogitEpi epi{&tm_e, a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.store != 0, a.check};
+  LogitEpi epi{&tm_e, a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.tn,
+               a.store != 0, a.check};
   gemm::run<0, 0>(&tm_h, &tm_w, a.shape, epi, a.check);
 }
 
@@ -157,60 +160,114 @@ logit_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ C
 // dH and dW
 // ----------------------------------------------------------------------------
 
-// bf16 output through the slab writer; or, for a dW that several chunks add up
-// to, fp32 sums in memory (`acc`): read when `add`, written back as fp32 unless
-// this is the last chunk, which writes bf16.
-struct GradEpi {
-  const CUtensorMap* tm_out;
+// What dH's rows still need: P's entry at the target, the largest of the row for
+// most tokens, enters the product as bf16; what that rounding took off comes
+// back here, times the target's row of W, in fp32.
+struct TargetRest {
+  const float* rest;        // [T] fp32 minus bf16 of P's target entry, or nullptr
+  const uint16_t* W;
+  const void* target;
+  int target64;
+  int64_t V, d, ignore_index;
+
+  __device__ __forceinline__ const uint16_t* row(int64_t t, float& r, unsigned int* check) const {
+    r = 0.f;
+    if (rest == nullptr) return nullptr;
+    const int64_t y = class_of(target, target64, t, V, ignore_index, check);
+    if (y < 0) return nullptr;
+    r = rest[t];
+    return W + y * d;
+  }
+};
+
+__device__ __forceinline__ void add_scaled8(float (&f)[8], const uint16_t* w, float r) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(w));
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = fmaf(r, __uint_as_float(x[q] << 16), f[2 * q]);
+    f[2 * q + 1] = fmaf(r, __uint_as_float(x[q] & 0xffff0000u), f[2 * q + 1]);
+  }
+}
+
+// Where a gradient product's values go: bf16, or, for a dW that several chunks of
+// tokens add up to, fp32 sums in memory (`acc`): read when `add`, written back as
+// fp32 unless this is the last chunk, which writes bf16.
+struct GradOut {
   float* acc;
   int add, last;
   int64_t M, N;
+  TargetRest rest;
 
-  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, int warp, int lane, gemm::SlabWriter& out) {
+  // eight columns of a row (N % 8 == 0: inside or outside as a whole)
+  __device__ __forceinline__ void finish(float (&f)[8], int64_t row, int64_t col, const uint16_t* wrow, float r) const {
+    if (wrow != nullptr) add_scaled8(f, wrow + col, r);
+    if (acc != nullptr) {
+      float4* p = reinterpret_cast<float4*>(acc + row * N + col);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (add) {
+          const float4 g = p[h];
+          f[4 * h] += g.x;
+          f[4 * h + 1] += g.y;
+          f[4 * h + 2] += g.z;
+          f[4 * h + 3] += g.w;
+        }
+        if (!last) p[h] = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+      }
+    }
+  }
+};
+
+struct GradEpi {
+  const CUtensorMap* tm_out;
+  const GradOut& o;
+  float4* parts;            // [parts][2 CTAs][64 groups of 4 columns][128 rows]
+  unsigned int* check;
+
+  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, int part, int warp, int lane,
+                                       gemm::SlabWriter& out) {
     const int64_t row = m0 + 32 * warp + lane;
+    float r = 0.f;
+    const uint16_t* wrow = part < 0 && row < o.M ? o.rest.row(row, r, check) : nullptr;
 #pragma unroll 1
     for (int h = 0; h < gemm::TN / 64; ++h) {
       const int c0 = n0 + 64 * h;
-      if (c0 >= N) break;
-      uint32_t o[32];
+      if (c0 >= o.N) break;
+      uint32_t w[32];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         uint32_t v[32];
         tc::tmem_ld32(tmem + 64 * h + 32 * q, v);
         tc::tmem_ld_wait();
-        if (acc != nullptr && row < M) {
-          // d % 8 == 0: groups of eight columns are inside or outside as a whole
-          float4* p = reinterpret_cast<float4*>(acc + row * N + c0 + 32 * q);
+        if (part >= 0) {
+          float4* p = parts + ((int64_t)part * 2 + (m0 >> 7 & 1)) * 64 * 128 + (16 * h + 8 * q) * 128 + 32 * warp + lane;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (c0 + 32 * q + 4 * j >= N) break;
-            float4 f = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                   __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-            if (add) {
-              const float4 g = p[j];
-              f = make_float4(f.x + g.x, f.y + g.y, f.z + g.z, f.w + g.w);
-            }
-            if (!last) p[j] = f;
-            v[4 * j] = __float_as_uint(f.x);
-            v[4 * j + 1] = __float_as_uint(f.y);
-            v[4 * j + 2] = __float_as_uint(f.z);
-            v[4 * j + 3] = __float_as_uint(f.w);
-          }
+          for (int j = 0; j < 8; ++j)
+            p[j * 128] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                     __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+          continue;
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          o[16 * q + j] = f32x2_to_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        for (int j = 0; j < 4; ++j) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * j + e]);
+          const int64_t col = c0 + 32 * q + 8 * j;
+          if (row < o.M && col < o.N) o.finish(f, row, col, wrow, r);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[16 * q + 4 * j + e] = f32x2_to_bf16x2(f[2 * e], f[2 * e + 1]);
+        }
       }
-      if ((acc == nullptr || last) && m0 + 32 * warp < M) out.put(tm_out, o, c0, m0 + 32 * warp, lane);
+      if (part < 0 && (o.acc == nullptr || o.last) && m0 + 32 * warp < o.M) out.put(tm_out, w, c0, m0 + 32 * warp, lane);
     }
   }
 };
 
 struct GradArgs {
   gemm::Shape shape;
-  float* acc;
-  int add, last;
-  int64_t M, N;
+  GradOut out;
+  float4* parts;
   unsigned int* check;
 };
 
@@ -218,9 +275,41 @@ struct GradArgs {
 template <int A_MN>
 __global__ void __launch_bounds__(gemm::THREADS, 1)
 grad_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-            const __grid_constant__ CUtensorMap tm_out, GradArgs a) {
-  GradEpi epi{&tm_out, a.acc, a.add, a.last, a.M, a.N};
+            const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ GradArgs a) {
+  GradEpi epi{&tm_out, a.out, a.parts, a.check};
   gemm::run<A_MN, 1>(&tm_a, &tm_b, a.shape, epi, a.check);
+}
+
+// Joins the parts of the tiles that were cut along K, in part order: block
+// (tile, CTA half, group of 64 columns), thread = (row, 32 columns).
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ GradArgs a, uint16_t* __restrict__ out) {
+  const gemm::Shape& s = a.shape;
+  int m, n;
+  gemm::tile_at(s, s.split_from + blockIdx.x, m, n);
+  const int r128 = threadIdx.x & 127, half = threadIdx.x >> 7;
+  const int64_t row = (int64_t)m * gemm::TM + 128 * blockIdx.y + r128;
+  const int64_t col0 = (int64_t)n * gemm::TN + 64 * blockIdx.z + 32 * half;
+  if (row >= a.out.M) return;
+  float r;
+  const uint16_t* wrow = a.out.rest.row(row, r, a.check);
+  const float4* p = a.parts + ((int64_t)blockIdx.x * s.split * 2 + blockIdx.y) * 64 * 128 +
+                    (16 * blockIdx.z + 8 * half) * 128 + r128;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t col = col0 + 8 * j;
+    if (col >= a.out.N) break;
+    float f[8] = {};
+    for (int q = 0; q < s.split; ++q) {
+      const float4 x = p[(int64_t)q * 2 * 64 * 128 + (2 * j) * 128], y = p[(int64_t)q * 2 * 64 * 128 + (2 * j + 1) * 128];
+      f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+      f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+    }
+    a.out.finish(f, row, col, wrow, r);
+    if (a.out.acc == nullptr || a.out.last)
+      *reinterpret_cast<uint4*>(out + row * a.out.N + col) =
+          make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
+                     f32x2_to_bf16x2(f[6], f[7]));
+  }
 }
 
 // ----------------------------------------------------------------------------
@@ -244,8 +333,17 @@ __global__ void __launch_bounds__(1024) count_kernel(const void* target, int tar
   }
 }
 
-// lse and loss of 32 tokens per block: eight thread rows walk the vocabulary's
-// tiles and join (maximum, sum) pairs, then the eight pairs are joined in order.
+// Join (maximum, sum of exponentials) pairs.  fmaxf drops a NaN maximum, but a
+// tile with a NaN logit has a NaN sum, which stays.
+__device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  const float base = top == -INFINITY ? 0.f : top;
+  s = s * expf(m - base) + s2 * expf(m2 - base);
+  m = top;
+}
+
+// lse and loss of eight tokens per block: 32 thread rows walk the vocabulary's
+// tiles, then their pairs are joined by halves.
 // The loss is (maximum - l_target) + log(sum): next to lse - l_target it keeps the
 // digits of a surely predicted token, whose maximum is the target's own logit.
 // nll: the target's logits in, the losses out.
@@ -253,27 +351,27 @@ __global__ void __launch_bounds__(256) lse_kernel(const float2* __restrict__ sta
                                                   const void* target, int target64, int64_t ignore, int T, int64_t V,
                                                   int tiles, float* __restrict__ lse, float* __restrict__ losses,
                                                   unsigned int* check) {
-  __shared__ float2 joined[8][32];
-  const int t = blockIdx.x * 32 + threadIdx.x;
+  __shared__ float2 joined[32][8];
+  const int t = blockIdx.x * 8 + threadIdx.x, y = threadIdx.y;
   float m = -INFINITY, s = 0.f;
-  auto join = [](float& m, float& s, float m2, float s2) {
-    // a NaN maximum (fmaxf drops it) still arrives through the sum
-    const float top = fmaxf(m, m2);
-    const float base = top == -INFINITY ? 0.f : top;
-    s = s * expf(m - base) + s2 * expf(m2 - base);
-    m = top;
-  };
   if (t < T) {
 #pragma unroll 4
-    for (int i = threadIdx.y; i < tiles; i += 8) {
+    for (int i = y; i < tiles; i += 32) {
       const float2 p = stats[(int64_t)i * T + t];
-      join(m, s, p.x, p.y);
+      join_stats(m, s, p.x, p.y);
     }
   }
-  joined[threadIdx.y][threadIdx.x] = make_float2(m, s);
-  __syncthreads();
-  if (threadIdx.y == 0 && t < T) {
-    for (int q = 1; q < 8; ++q) join(m, s, joined[q][threadIdx.x].x, joined[q][threadIdx.x].y);
+  joined[y][threadIdx.x] = make_float2(m, s);
+#pragma unroll
+  for (int half = 16; half > 0; half >>= 1) {
+    __syncthreads();
+    if (y < half) {
+      const float2 o = joined[y + half][threadIdx.x];
+      join_stats(m, s, o.x, o.y);
+      joined[y][threadIdx.x] = make_float2(m, s);
+    }
+  }
+  if (y == 0 && t < T) {
     const float ls = logf(s);
     lse[t] = m + ls;
     const float loss = class_of(target, target64, t, V, ignore, check) >= 0 ? (m - nll[t]) + ls : 0.f;
@@ -315,6 +413,7 @@ struct ProbArgs {
   const float* dloss;
   int dloss_each;           // dloss has one value per token
   const int64_t* count;     // divide by it (mean), or nullptr
+  float* rest;              // [T]: P's target entry minus its bf16
   unsigned int* check;
 };
 
@@ -334,6 +433,7 @@ __global__ void __launch_bounds__(kProbThreads) prob_kernel(ProbArgs a) {
   if (a.count != nullptr) c /= (float)(*a.count > 0 ? *a.count : 1);
   const float z = a.lse[t];
   const float at_target = c * expm1f(-a.nll[t]);
+  if (threadIdx.x == 0) a.rest[t] = at_target - __bfloat162float(__float2bfloat16_rn(at_target));
   // a warp's 32 units of eight columns are one 256-column tile: one factor per warp and step
   for (int u = threadIdx.x; u < units; u += kProbThreads) {
     const float f = c * __expf(a.stats[(int64_t)(u >> 5) * a.T + t].x - z);
@@ -382,7 +482,7 @@ int64_t chunk_tokens(int64_t T, int64_t V, bool grads) {
 
 struct Layout {
   int64_t chunk, pitch;
-  size_t e, acc, stats, lse, nll, losses, count, total;
+  size_t e, acc, parts, stats, lse, nll, rest, losses, count, total;
 };
 
 Layout layout(int64_t T, int64_t V, int64_t d, bool dh, bool dw) {
@@ -398,9 +498,11 @@ Layout layout(int64_t T, int64_t V, int64_t d, bool dh, bool dw) {
   };
   l.e = take(grads ? (size_t)l.chunk * l.pitch * 2 : 0);
   l.acc = take(dw && l.chunk < T ? (size_t)V * d * 4 : 0);
-  l.stats = take((size_t)tiles_of(V) * l.chunk * 8);
+  l.parts = take(grads ? (size_t)(num_sms() / 2) * gemm::TM * gemm::TN * 4 : 0);
+  l.stats = take((size_t)((V + kMinTile - 1) / kMinTile) * l.chunk * 8);
   l.lse = take((size_t)l.chunk * 4);
   l.nll = take((size_t)l.chunk * 4);
+  l.rest = take((size_t)l.chunk * 4);
   l.losses = take((size_t)T * 4);
   l.count = take(8);
   l.total = at;
@@ -418,7 +520,7 @@ cudaError_t launch_pairs(Kern kern, const CUtensorMap& ma, const CUtensorMap& mb
                          cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm::SMEM);
   if (e != cudaSuccess) return e;
-  const int tiles = args.shape.mt * args.shape.nt, pairs = num_sms() / 2;
+  const int tiles = gemm::items(args.shape), pairs = num_sms() / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)(tiles < pairs ? tiles : pairs), 1, 1);
   cfg.blockDim = dim3(gemm::THREADS, 1, 1);
@@ -440,8 +542,49 @@ gemm::Shape shape_of(int64_t M, int64_t N, int64_t K) {
   s.mt = (int)tiles_of(M);
   s.nt = (int)tiles_of(N);
   s.ksteps = (int)((K + gemm::KS - 1) / gemm::KS);
+  s.tn = gemm::TN;
   s.group = s.mt < 16 ? s.mt : 16;
+  s.split_from = s.mt * s.nt;
+  s.split = 1;
   return s;
+}
+
+// The loss alone: classes per tile.  The pairs take the tiles in rounds, and few
+// tokens make few tiles, so a tile is narrowed until the last round is as full as
+// the others (the time goes with rounds * width).
+void balance_tiles(gemm::Shape& s, int64_t V) {
+  const int64_t pairs = num_sms() / 2;
+  int64_t best = 0;
+  for (int tn = gemm::TN; tn >= kMinTile; tn -= 32) {
+    const int64_t nt = (V + tn - 1) / tn, rounds = (s.mt * nt + pairs - 1) / pairs;
+    if (best == 0 || rounds * tn < best) {
+      best = rounds * tn;
+      s.tn = tn;
+      s.nt = (int)nt;
+    }
+  }
+  s.split_from = s.mt * s.nt;
+}
+
+// A gradient product: cut the tiles of the last, partly filled round along K so
+// that every pair has a part.  Worth a second launch that joins the parts only
+// when it shortens the round by more than that launch takes (about 32 K steps of
+// a quarter of a microsecond).
+void split_last_round(gemm::Shape& s) {
+  const int pairs = num_sms() / 2, tiles = s.mt * s.nt, rem = tiles % pairs;
+  if (rem == 0) return;
+  int split = pairs / rem;
+  if (split > 8) split = 8;
+  if (split < 2 || s.ksteps - s.ksteps / split < 32) return;
+  s.split_from = tiles - rem;
+  s.split = split;
+}
+
+cudaError_t launch_join(const GradArgs& a, uint16_t* out, cudaStream_t s) {
+  const int cut = a.shape.mt * a.shape.nt - a.shape.split_from;
+  if (cut == 0) return cudaSuccess;
+  join_kernel<<<dim3((unsigned)cut, 2, 4), 256, 0, s>>>(a, out);
+  return cudaGetLastError();
 }
 
 #define SK_TRY(x)                       \
@@ -465,6 +608,8 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
   float2* stats = reinterpret_cast<float2*>(ws + l.stats);
   float* lse = reinterpret_cast<float*>(ws + l.lse);
   float* nll = reinterpret_cast<float*>(ws + l.nll);
+  float* rest = reinterpret_cast<float*>(ws + l.rest);
+  float4* parts = reinterpret_cast<float4*>(ws + l.parts);
   float* losses = a.reduction == SK_CE_NONE ? a.loss : reinterpret_cast<float*>(ws + l.losses);
   int64_t* count = reinterpret_cast<int64_t*>(ws + l.count);
   const bool mean = a.reduction == SK_CE_MEAN;
@@ -472,11 +617,9 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     count_kernel<<<1, 1024, 0, s>>>(a.target, a.target64, a.T, a.V, a.ignore_index, a.check, count);
     SK_TRY(cudaGetLastError());
   }
-  CUtensorMap tm_w, tm_w_mn, tm_dw;
-  SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, 128));
+  CUtensorMap tm_w_mn, tm_dw;
   if (dh) SK_TRY(map_rows(&tm_w_mn, a.W, a.V, a.d, a.d, 64, 64));
   if (dw) SK_TRY(map_rows(&tm_dw, a.dW, a.V, a.d, a.d, 64, 32));
-  const int vt = (int)tiles_of(a.V);
   for (int64_t t0 = 0; t0 < a.T; t0 += l.chunk) {
     const int64_t T = a.T - t0 < l.chunk ? a.T - t0 : l.chunk;
     const uint16_t* H = a.H + t0 * a.d;
@@ -485,32 +628,41 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     SK_TRY(map_rows(&tm_h, H, T, a.d, a.d, 64, 128));
     tm_e = tm_h;                                   // not used without gradients
     if (grads) SK_TRY(map_rows(&tm_e, E, T, a.V, l.pitch, 64, 32));
-    LogitArgs la{shape_of(T, a.V, a.d), stats, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
+    gemm::Shape shape = shape_of(T, a.V, a.d);
+    if (!grads) balance_tiles(shape, a.V);
+    CUtensorMap tm_w;
+    SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, shape.tn / 2));
+    LogitArgs la{shape, stats, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
                  grads ? 1 : 0, a.check};
     SK_TRY(launch_pairs(logit_kernel, tm_h, tm_w, tm_e, la, s));
-    lse_kernel<<<(unsigned)((T + 31) / 32), dim3(32, 8), 0, s>>>(stats, nll, target, a.target64, a.ignore_index,
-                                                                 (int)T, a.V, vt, lse, losses ? losses + t0 : nullptr,
+    lse_kernel<<<(unsigned)((T + 7) / 8), dim3(8, 32), 0, s>>>(stats, nll, target, a.target64, a.ignore_index,
+                                                                 (int)T, a.V, shape.nt, lse, losses ? losses + t0 : nullptr,
                                                                  a.check);
     SK_TRY(cudaGetLastError());
     if (!grads) continue;
     const bool each = a.reduction == SK_CE_NONE;
     ProbArgs pa{E, l.pitch, stats, lse, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
-                each && a.dloss ? a.dloss + t0 : a.dloss, each ? 1 : 0, mean ? count : nullptr, a.check};
+                each && a.dloss ? a.dloss + t0 : a.dloss, each ? 1 : 0, mean ? count : nullptr, rest, a.check};
     prob_kernel<<<(unsigned)T, kProbThreads, 0, s>>>(pa);
     SK_TRY(cudaGetLastError());
     if (dh) {
       CUtensorMap tm_p, tm_dh;
       SK_TRY(map_rows(&tm_p, E, T, a.V, l.pitch, 64, 128));
       SK_TRY(map_rows(&tm_dh, a.dH + t0 * a.d, T, a.d, a.d, 64, 32));
-      GradArgs ga{shape_of(T, a.d, a.V), nullptr, 0, 1, T, a.d, a.check};
+      GradArgs ga{shape_of(T, a.d, a.V),
+                  {nullptr, 0, 1, T, a.d, {rest, a.W, target, a.target64, a.V, a.d, a.ignore_index}}, parts, a.check};
+      split_last_round(ga.shape);
       SK_TRY(launch_pairs(grad_kernel<0>, tm_p, tm_w_mn, tm_dh, ga, s));
+      SK_TRY(launch_join(ga, a.dH + t0 * a.d, s));
     }
     if (dw) {
       CUtensorMap tm_p, tm_hm;
       SK_TRY(map_rows(&tm_p, E, T, a.V, l.pitch, 64, 64));
       SK_TRY(map_rows(&tm_hm, H, T, a.d, a.d, 64, 64));
-      GradArgs ga{shape_of(a.V, a.d, T), acc, t0 > 0 ? 1 : 0, t0 + T >= a.T ? 1 : 0, a.V, a.d, a.check};
+      GradArgs ga{shape_of(a.V, a.d, T), {acc, t0 > 0 ? 1 : 0, t0 + T >= a.T ? 1 : 0, a.V, a.d, {}}, parts, a.check};
+      split_last_round(ga.shape);
       SK_TRY(launch_pairs(grad_kernel<1>, tm_p, tm_hm, tm_dw, ga, s));
+      SK_TRY(launch_join(ga, a.dW, s));
     }
   }
   if (a.reduction != SK_CE_NONE && a.loss != nullptr) {

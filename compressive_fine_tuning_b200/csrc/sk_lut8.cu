@@ -32,6 +32,7 @@ constexpr int SMEM = 1024 + BAR_OFF + 256;
 constexpr int PRODUCERS = 8, TMA_WARP = 8, MMA_WARP = 9, THREADS = 320;
 constexpr uint32_t IDESC = tc::idesc_bf16(256, N, 1, 1);
 constexpr int TMEM_COLS = 256;
+constexpr int COPIES = 4;             // copies of the bins in the epilogue
 static_assert(PRODUCERS * 8 == KS, "a producer warp fills one K-group of eight tokens");
 
 __host__ __device__ constexpr int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
@@ -60,7 +61,7 @@ struct Lut8Args {
   int row_pairs;
 };
 
-template <int BITS>
+template <int BITS, bool ROUTED>
 __global__ void __launch_bounds__(THREADS, 2) lut8_tc_kernel(const __grid_constant__ CUtensorMap tm_dy, Lut8Args a) {
   constexpr int K = 1 << BITS;
   extern __shared__ uint8_t smem_raw[];
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(THREADS, 2) lut8_tc_kernel(const __grid_consta
   const int64_t i0 = (int64_t)((int)blockIdx.z - set * a.row_pairs) * 256 + 128 * rank;
   int k_first = 0;
   int tokens = (int)a.T;
-  if (a.segs != nullptr) {
+  if constexpr (ROUTED) {
     k_first = a.segs[2 * set];
     tokens = a.segs[2 * set + 1];
   }
@@ -152,91 +153,117 @@ __global__ void __launch_bounds__(THREADS, 2) lut8_tc_kernel(const __grid_consta
     // columns 32 h .. 32 h + 31 of this CTA's 128
     const int r8 = lane & 7, h = lane >> 3;
     const int lr = 8 * warp + r8;
+    // the epilogue warps' row indices of this column tile, loaded while the MMAs
+    // run so that their memory latency is off the binning loop
+    const int64_t row_i = i0 + threadIdx.x;
+    Chunk<BITS> chunks[N / 32] = {};
+    if (warp < 4 && row_i < a.n) {
+#pragma unroll
+      for (int b = 0; b < N / 32; ++b)
+        if (j0 + 32 * b < a.d) chunks[b] = load_chunk<BITS>(a.packed + row_i * a.row_bytes, (j0 >> 5) + b);
+    }
     const int64_t j = j0 + 128 * rank + 32 * h;
     const bool col_ok = j < a.d;
     const int64_t sblocks = a.d >> 5;
-    uint32_t slot_off[2][2];           // 16-byte swizzled slots of the block's four bf16 quarters
+    uint32_t slot_off[4];              // 16-byte swizzled slots of the block's four bf16 quarters
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      slot_off[e >> 1][e & 1] = (h >> 1) * 8192 + warp * 1024 + r8 * 128 + (((4 * (h & 1) + e) ^ r8) << 4);
+      slot_off[e] = (h >> 1) * 8192 + warp * 1024 + r8 * 128 + (((4 * (h & 1) + e) ^ r8) << 4);
+    // 32 bytes and a scale byte per step, loaded two steps ahead; a position's
+    // token (one LUT set: the position itself) is known one step before that
+    const int8_t* q_col = a.q + j;
+    const uint8_t* s_col = a.scale + (j >> 5);
     auto token_of = [&](int i) -> int {
       const int t = i * KS + lr;
-      if (i >= nsteps || t >= tokens || !col_ok) return -1;
-      return a.perm != nullptr ? __ldg(a.perm + k_first + t) : t;
+      if (t >= tokens || !col_ok) return -1;
+      return ROUTED ? __ldg(a.perm + k_first + t) : t;
     };
-    uint4 q0n = make_uint4(0u, 0u, 0u, 0u), q1n = q0n;
-    uint32_t byten = 0u;
-    auto fetch = [&](int t) {
+    struct Block {
+      uint4 q0, q1;
+      uint32_t byte;
+    };
+    auto fetch = [&](int t) -> Block {
+      Block b{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u), 0u};   // zero scale: the tile's padding is zero
       if (t >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)t * a.d + j);
-        q0n = __ldg(src);
-        q1n = __ldg(src + 1);
-        byten = __ldg(a.scale + (int64_t)t * sblocks + (j >> 5));
-      } else {
-        q0n = q1n = make_uint4(0u, 0u, 0u, 0u);
-        byten = 0u;                   // zero scale: the tile's padding is zero
+        const uint4* src = reinterpret_cast<const uint4*>(q_col + (int64_t)t * a.d);
+        b.q0 = __ldg(src);
+        b.q1 = __ldg(src + 1);
+        b.byte = __ldg(s_col + (int64_t)t * sblocks);
       }
+      return b;
     };
-    fetch(token_of(0));
-    int tok = token_of(1);            // tokens run one step ahead of their values
+    Block ahead[2] = {fetch(token_of(0)), fetch(token_of(1))};
+    int tok = token_of(2);
     const uint32_t full_b_even = tc::mapa(&full_b[0], 0);
-    for (int i = 0; i < nsteps; ++i) {
-      const uint4 q0 = q0n, q1 = q1n;
-      const float sc = __uint_as_float(byten << 23);
-      fetch(tok);
-      tok = token_of(i + 2);
-      uint4 o[4];
-      ckpt8_dequant4(q0.x, sc, o[0].x, o[0].y);
-      ckpt8_dequant4(q0.y, sc, o[0].z, o[0].w);
-      ckpt8_dequant4(q0.z, sc, o[1].x, o[1].y);
-      ckpt8_dequant4(q0.w, sc, o[1].z, o[1].w);
-      ckpt8_dequant4(q1.x, sc, o[2].x, o[2].y);
-      ckpt8_dequant4(q1.y, sc, o[2].z, o[2].w);
-      ckpt8_dequant4(q1.z, sc, o[3].x, o[3].y);
-      ckpt8_dequant4(q1.w, sc, o[3].z, o[3].w);
-      const int s = i % S;
-      if (*abort_flag || !tc::mbar_wait(&empty[s], ((i / S) & 1) ^ 1, a.check)) { *abort_flag = 1; break; }
-      uint8_t* bt = smem + s * STAGE + A_BYTES;
+    bool ok = true;
+#pragma unroll 1
+    for (int i0s = 0; i0s < nsteps && ok; i0s += 2) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(bt + slot_off[e >> 1][e & 1]) = o[e];
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(full_b_even + 8 * s);
+      for (int half = 0; half < 2; ++half) {
+        const int i = i0s + half;
+        if (i >= nsteps || !ok) break;
+        const Block cur = ahead[half];
+        ahead[half] = fetch(tok);
+        tok = token_of(i + 3);
+        const uint32_t s2 = ckpt8_scale2(cur.byte);
+        uint4 o[4];
+        ckpt8_dequant4(cur.q0.x, s2, o[0].x, o[0].y);
+        ckpt8_dequant4(cur.q0.y, s2, o[0].z, o[0].w);
+        ckpt8_dequant4(cur.q0.z, s2, o[1].x, o[1].y);
+        ckpt8_dequant4(cur.q0.w, s2, o[1].z, o[1].w);
+        ckpt8_dequant4(cur.q1.x, s2, o[2].x, o[2].y);
+        ckpt8_dequant4(cur.q1.y, s2, o[2].z, o[2].w);
+        ckpt8_dequant4(cur.q1.z, s2, o[3].x, o[3].y);
+        ckpt8_dequant4(cur.q1.w, s2, o[3].z, o[3].w);
+        const int s = i % S;
+        if (*abort_flag || !tc::mbar_wait(&empty[s], ((i / S) & 1) ^ 1, a.check)) { *abort_flag = 1; ok = false; break; }
+        uint8_t* bt = smem + s * STAGE + A_BYTES;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(bt + slot_off[e]) = o[e];
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(full_b_even + 8 * s);
+      }
     }
     if (warp < 4) {
       // epilogue: thread = row i (TMEM lane); bin the row's 256 columns
       __syncwarp();
-      float* bins = reinterpret_cast<float*>(smem + BAR_OFF - K * 128 * 4);  // [K][128], tail of stage memory
-      const int tid = threadIdx.x;                                         // 0..127
-      const int64_t i = i0 + tid;
-      const uint8_t* row = a.packed + i * a.row_bytes;
-      Chunk<BITS> ch{};
-      if (i < a.n) ch = load_chunk<BITS>(row, j0 >> 5);
+      // [COPIES][K][128], tail of stage memory: consecutive columns add into different
+      // copies, so their loads do not wait for one another's stores
+      float* bins = reinterpret_cast<float*>(smem + BAR_OFF - COPIES * K * 128 * 4) + threadIdx.x;
       bool have = !*abort_flag && tc::mbar_wait(d_full, 0, a.check) && nsteps > 0;   // no steps: nothing accumulated
       have = __all_sync(0xffffffffu, have);  // tcgen05.ld is warp-collective
       if (have) tc::tc_fence_after();
-      // the bins reuse the last stage's memory: every MMA has read it (d_full)
+      // the bins reuse the last stages' memory: every MMA has read it (d_full)
 #pragma unroll
-      for (int c = 0; c < K; ++c) bins[c * 128 + tid] = 0.f;
+      for (int c = 0; c < COPIES * K; ++c) bins[c * 128] = 0.f;
       const int first_g = (int)(j0 / a.gs);
       const int gs32 = (int)a.gs;
       int g = first_g, g_end = (first_g + 1) * gs32;
       bool dirty = false;
       auto flush = [&](int gg) {
-        if (i < a.n) {
-          float* dst = part + (((int64_t)jt * a.n + i) * a.slots + (gg - first_g)) * K;
+        float4* dst = reinterpret_cast<float4*>(part + (((int64_t)jt * a.n + row_i) * a.slots + (gg - first_g)) * K);
 #pragma unroll
-          for (int c = 0; c < K; ++c) dst[c] = bins[c * 128 + tid];
+        for (int c4 = 0; c4 < K / 4; ++c4) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = 4 * c4 + e;
+            v[e] = bins[c * 128];
+            bins[c * 128] = 0.f;
+#pragma unroll
+            for (int k = 1; k < COPIES; ++k) {
+              v[e] += bins[(k * K + c) * 128];
+              bins[(k * K + c) * 128] = 0.f;
+            }
+          }
+          if (row_i < a.n) dst[c4] = make_float4(v[0], v[1], v[2], v[3]);
         }
-#pragma unroll
-        for (int c = 0; c < K; ++c) bins[c * 128 + tid] = 0.f;
       };
-#pragma unroll 1
+#pragma unroll
       for (int b = 0; b < N / 32; ++b) {
         const int64_t jc = j0 + 32 * b;
         if (jc >= a.d) break;
-        const Chunk<BITS> cur = ch;
-        if (i < a.n && b + 1 < N / 32 && jc + 32 < a.d) ch = load_chunk<BITS>(row, (jc >> 5) + 1);
         uint32_t v[32];
         if (have) {
           tc::tmem_ld32(tc::tmem_addr(tmem, warp * 32, 32 * b), v);
@@ -250,9 +277,17 @@ __global__ void __launch_bounds__(THREADS, 2) lut8_tc_kernel(const __grid_consta
           do { ++g; g_end += gs32; } while ((int)jc >= g_end);
           dirty = false;
         }
-        if (i < a.n) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) bins[chunk_index<BITS>(cur, e) * 128 + tid] += __uint_as_float(v[e]);
+        for (int e = 0; e < 32; e += COPIES) {
+          float* at[COPIES];
+          float sum[COPIES];
+#pragma unroll
+          for (int k = 0; k < COPIES; ++k) {
+            at[k] = bins + (k * K + chunk_index<BITS>(chunks[b], e + k)) * 128;
+            sum[k] = *at[k];
+          }
+#pragma unroll
+          for (int k = 0; k < COPIES; ++k) *at[k] = sum[k] + __uint_as_float(v[e + k]);
         }
         dirty = true;
       }
@@ -272,29 +307,35 @@ __global__ void __launch_bounds__(THREADS, 2) lut8_tc_kernel(const __grid_consta
 }
 
 // Sum the partial bins of every (set, row, group) over the column tiles that
-// touch the group, in tile order, and write (or add to) dlut.
+// touch the group, in tile order, and write (or add to) dlut: four bins a thread.
 template <int BITS>
-__global__ void lut8_reduce_kernel(const float* __restrict__ part, int64_t n, int gpr, int64_t gs, int jtiles, int slots,
-                                   float* __restrict__ dlut, int accumulate, int64_t total, int64_t part_set_stride) {
-  constexpr int K = 1 << BITS;
-  const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+__global__ void __launch_bounds__(256) lut8_reduce_kernel(const float4* __restrict__ part, int64_t n, int gpr, int64_t gs,
+                                                          int jtiles, int slots, float4* __restrict__ dlut,
+                                                          int accumulate, int64_t total, int64_t part_set_stride) {
+  constexpr int Q = (1 << BITS) / 4;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (e >= total) return;
-  const int64_t per_set = n * gpr * K;
-  const int64_t set = e / per_set, es = e - set * per_set;
-  part += set * part_set_stride;
-  const int c = (int)(es % K);
-  const int64_t ig = es / K;
+  const int c = (int)(e % Q);
+  const int64_t ig = e / Q;
   const int g = (int)(ig % gpr);
-  const int64_t i = ig / gpr;
+  const int64_t si = ig / gpr, set = si / n, i = si - set * n;
+  part += set * part_set_stride;
   const int t_first = (int)(((int64_t)g * gs) / N);
   int t_last = (int)(((int64_t)(g + 1) * gs - 1) / N);
   if (t_last > jtiles - 1) t_last = jtiles - 1;
-  float sum = 0.f;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
   for (int t = t_first; t <= t_last; ++t) {
-    const int fg = (int)(((int64_t)t * N) / gs);
-    sum += part[(((int64_t)t * n + i) * slots + (g - fg)) * K + c];
+    // only a group's first tile can start in an earlier group
+    const int slot = t == t_first ? g - (int)(((int64_t)t * N) / gs) : 0;
+    const float4 v = __ldg(part + (((int64_t)t * n + i) * slots + slot) * Q + c);
+    sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
   }
-  dlut[e] = accumulate ? dlut[e] + sum : sum;
+  if (accumulate) {
+    const float4 o = dlut[e];
+    sum = make_float4(o.x + sum.x, o.y + sum.y, o.z + sum.z, o.w + sum.w);
+  }
+  dlut[e] = sum;
 }
 
 // ----------------------------------------------------------------------------
@@ -406,7 +447,7 @@ __global__ void __launch_bounds__(kBlock) lut8_simt_kernel(Problem p, const int8
         for (int64_t t = 0; t < p.T; ++t) {
           if (p.task != nullptr && token_task(p.task, t, p.ntask, p.check) != tau) continue;
           const uint32_t s2 = __ldg(dY + t * p.n + i);
-          const float sc = __uint_as_float((uint32_t)__ldg(scale + t * chunks + chunk) << 23);
+          const uint32_t sc = ckpt8_scale2(__ldg(scale + t * chunks + chunk));
           const uint4* xp = reinterpret_cast<const uint4*>(q + t * p.d + chunk * 32);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -512,14 +553,16 @@ cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* sca
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, kern, tm, args);
     if (err != cudaSuccess) return err;
-    red<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(part, p.n, p.gpr, p.gs, jtiles, slots, dlut, accumulate, total,
-                                                        stride);
+    const int64_t quads = total / 4;
+    red<<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(reinterpret_cast<const float4*>(part), p.n, p.gpr, p.gs, jtiles,
+                                                        slots, reinterpret_cast<float4*>(dlut), accumulate, quads,
+                                                        stride / 4);
     return cudaGetLastError();
   };
   switch (p.bits) {
-    case 2: return run(lut8_tc_kernel<2>, lut8_reduce_kernel<2>);
-    case 3: return run(lut8_tc_kernel<3>, lut8_reduce_kernel<3>);
-    default: return run(lut8_tc_kernel<4>, lut8_reduce_kernel<4>);
+    case 2: return routed ? run(lut8_tc_kernel<2, true>, lut8_reduce_kernel<2>) : run(lut8_tc_kernel<2, false>, lut8_reduce_kernel<2>);
+    case 3: return routed ? run(lut8_tc_kernel<3, true>, lut8_reduce_kernel<3>) : run(lut8_tc_kernel<3, false>, lut8_reduce_kernel<3>);
+    default: return routed ? run(lut8_tc_kernel<4, true>, lut8_reduce_kernel<4>) : run(lut8_tc_kernel<4, false>, lut8_reduce_kernel<4>);
   }
 }
 

@@ -108,7 +108,10 @@ def test_lut_gradient(n, d, bits, gpr, T, sets):
     acc = sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, task, sets, out=start.clone(), accumulate=True)
     assert torch.equal(acc, start + got)
     if sets == 1 and T >= 64:
-        assert torch.equal(got, sk.linear_bwd_lut(packed, bits, gpr, sk.ckpt8_dequant(ck), dY))
+        # the same products and accumulations as the bf16 gradient of the same values;
+        # only the order of the 256-column binning (and its tiles' joining) differs
+        same = sk.linear_bwd_lut(packed, bits, gpr, sk.ckpt8_dequant(ck), dY)
+        assert (np.abs((got - same).cpu().numpy()) <= lim * (1024 * 2.0 ** -24) / ((T / 16 + 512) * 2.0 ** -23)).all()
     assert sk.device_check() == 0
 
 
@@ -199,7 +202,7 @@ def test_layer_with_checkpoint():
         grads.append(m.lut.grad.clone())
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
     assert torch.equal(xs[0].grad, xs[1].grad) and torch.equal(xs[0].grad, xs[2].grad)
-    want = sk.linear_bwd_lut(packed, 4, 2, sk.ckpt8_dequant(sk.ckpt8(X)), dY)
+    want = sk.linear_bwd_lut_ckpt8(packed, 4, 2, sk.ckpt8(X), dY)
     assert torch.equal(grads[1], want) and torch.equal(grads[2], want)
     # the checkpoint moves the gradient by no more than its rounding: 2^(e-1) per value
     step = np.repeat(2.0 ** (sk.ckpt8(X).scale.cpu().numpy().astype(np.float64) - 128.0), 32, axis=1)

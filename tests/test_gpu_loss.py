@@ -80,9 +80,15 @@ def test_loss_and_gradients(T, V, d, reduction):
     _check(dH, rh, lim_h, "dH")
     _check(dW, rw, lim_w, "dW")
     assert not _n(dH)[~keep].any()
-    # each output alone, the same inputs again: the same numbers
+    # The loss alone may cut the vocabulary into narrower tiles: another order of fewer
+    # than 64 additions of 2^-24 on either side (2^-17 of the sum, absolute in its
+    # logarithm) and the roundings of the largest logit's size.
     l2, a, b = sk.cross_entropy(hd, wd, yd, reduction=reduction)
-    assert a is None and b is None and torch.equal(l2, loss)
+    assert a is None and b is None
+    near = 2.0 ** -17 + 2.0 ** -22 * np.abs(H @ W.T).max()
+    assert np.abs(_n(l2) - _n(loss)).max() <= near * (max(1, keep.sum()) if reduction == "sum" else 1)
+    assert torch.equal(l2, sk.cross_entropy(hd, wd, yd, reduction=reduction)[0])
+    # each gradient alone, the same inputs again: the same numbers
     dlc = None if dl is None else dl.cuda()
     assert torch.equal(sk.cross_entropy(hd, wd, yd.int(), reduction=reduction, dloss=dlc, need_loss=False, need_dh=True)[1], dH)
     assert torch.equal(sk.cross_entropy(hd, wd, yd, reduction=reduction, dloss=dlc, need_loss=False, need_dw=True)[2], dW)
@@ -177,7 +183,8 @@ def test_autograd():
     wd = w.cuda().requires_grad_()
     yd = y.cuda().reshape(3, 20)
     loss = sk.linear_cross_entropy(hd, wd, yd)
-    assert torch.equal(loss, sk.linear_cross_entropy(hd.detach(), wd.detach(), yd))
+    alone = sk.linear_cross_entropy(hd.detach(), wd.detach(), yd)
+    assert abs(float(alone) - float(loss)) <= 2.0 ** -17 + 2.0 ** -22 * np.abs(_n(h) @ _n(w).T).max()
     one = torch.autograd.grad(loss, [hd, wd], retain_graph=True)
     kept = [t.clone() for t in one]
     two = torch.autograd.grad(loss * 4.0, [hd, wd], retain_graph=True)

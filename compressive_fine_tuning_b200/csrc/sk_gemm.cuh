@@ -19,13 +19,22 @@ namespace gemm {
 constexpr int TM = 256, TN = 256, KS = 64;
 constexpr int A_BYTES = 128 * KS * 2, B_BYTES = 128 * KS * 2, STAGE = A_BYTES + B_BYTES;
 constexpr int S = 6;
-constexpr int EPI_WARPS = 4, TMA_WARP = 4, MMA_WARP = 5, THREADS = 192;
 constexpr int SLAB = 32 * 128;                    // one warp's output slab: 32 rows x 128 bytes
-constexpr int SLAB_OFF = S * STAGE;               // two slabs per epilogue warp
-constexpr int BAR_OFF = SLAB_OFF + EPI_WARPS * 2 * SLAB;
+constexpr int SCRATCH_OFF = S * STAGE;            // the epilogue's own memory (two slabs for each of four warps)
+constexpr int SCRATCH = 8 * SLAB;
+constexpr int BAR_OFF = SCRATCH_OFF + SCRATCH;
 constexpr int SMEM = 1024 + BAR_OFF + 256;
 constexpr int TMEM_COLS = 512;
 static_assert(SMEM <= 232448, "one CTA's shared memory");
+
+// EW epilogue warps (4 or 8: warps w and w + 4 see the same accumulator rows),
+// then one warp for the copies and one for the MMAs.
+__host__ __device__ constexpr int threads(int ew) { return 32 * (ew + 2); }
+
+struct Item {
+  int m, n, k0, k1;      // tile, and the K steps [k0, k1) that it sums (none: see Epi)
+  int part;              // -1: a whole tile
+};
 
 struct Shape {
   int mt, nt, ksteps;    // tiles and K steps
@@ -36,11 +45,6 @@ struct Shape {
   // busy for a whole tile while the others idle.  A part's accumulator goes to the
   // epilogue with its index; the caller joins the parts.
   int split_from, split;
-};
-
-struct Item {
-  int m, n, k0, k1;
-  int part;              // -1: a whole tile
 };
 
 __host__ __device__ inline int items(const Shape& s) {
@@ -56,6 +60,13 @@ __host__ __device__ inline void tile_at(const Shape& s, int i, int& m, int& n) {
   const int rows = left < s.group ? left : s.group;
   n = r / rows;
   m = band * s.group + (r - n * rows);
+}
+
+// the inverse of tile_at
+__host__ __device__ inline int tile_index(const Shape& s, int m, int n) {
+  const int band = m / s.group, left = s.mt - band * s.group;
+  const int rows = left < s.group ? left : s.group;
+  return band * s.group * s.nt + n * rows + (m - band * s.group);
 }
 
 __device__ __forceinline__ Item item_at(const Shape& s, int i) {
@@ -80,10 +91,10 @@ __device__ __forceinline__ Item item_at(const Shape& s, int i) {
 // the matrix).  Slabs alternate; a slab is written again only after the store
 // before the last one has read it.
 struct SlabWriter {
-  uint8_t* base;      // this warp's two slabs
-  int at;
-  __device__ __forceinline__ void put(const CUtensorMap* map, const uint32_t (&w)[32], int x, int y, int lane) {
-    uint8_t* slab = base + (at & 1) * SLAB;
+  int at = 0;
+  __device__ __forceinline__ void put(uint8_t* scratch, const CUtensorMap* map, const uint32_t (&w)[32], int x, int y,
+                                      int warp, int lane) {
+    uint8_t* slab = scratch + (2 * warp + (at & 1)) * SLAB;
     ++at;
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
     __syncwarp();
@@ -105,15 +116,29 @@ struct SlabWriter {
   }
 };
 
-// Epi: struct with
-//   void tile(uint32_t tmem, int m0, int n0, int part, int warp, int lane, SlabWriter&)
-// called by every epilogue warp for every item: the warp's accumulator rows are
-// m0 + 32 warp + lane (TMEM lanes), columns n0 .. n0 + tn - 1.
-template <int A_MN, int B_MN, class Epi>
-__device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* tm_b, const Shape& sh, Epi& epi,
+// The items of one product.  Another plan has the same three members.
+struct Plan {
+  const Shape& s;
+  __device__ __forceinline__ int count() const { return items(s); }
+  __device__ __forceinline__ int tn() const { return s.tn; }
+  __device__ __forceinline__ Item item(int i) const { return item_at(s, i); }
+};
+
+// Epi: struct with, for every epilogue warp and item,
+//   void ready(const Item&, int m0, int n0, int warp, int lane)
+// before the accumulator is waited for (loads that the tile will need), and
+//   void tile(uint32_t tmem, int m0, int n0, const Item&, int warp, int lane, uint8_t* scratch)
+// when it is final: the warp's accumulator rows are m0 + 32 (warp % 4) + lane (TMEM
+// lanes), columns n0 .. n0 + tn - 1; an item without K steps has no accumulator.
+//   void done(int lane)
+// once, before the CTA leaves.  `scratch` is the 32 KB of shared memory that the
+// epilogue has to itself.
+template <int A_MN, int B_MN, int EW, class P, class Epi>
+__device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* tm_b, const P& plan, Epi& epi,
                                     unsigned int* check) {
-  const uint32_t idesc = tc::idesc_bf16(TM, B_MN ? TN : sh.tn, A_MN, B_MN);
-  const int tn = B_MN ? TN : sh.tn, half_n = tn / 2;
+  constexpr int TMA_WARP = EW, MMA_WARP = EW + 1;
+  const int tn = B_MN ? TN : plan.tn(), half_n = tn / 2;
+  const uint32_t idesc = tc::idesc_bf16(TM, tn, A_MN, B_MN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + BAR_OFF);   // even CTA: both CTAs' operands landed
@@ -126,7 +151,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
   const int warp = tc::warp_id(), lane = tc::lane_id();
   const int rank = (int)tc::cluster_ctarank();                     // 0: issues the MMAs
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int count = items(sh);
+  const int count = plan.count();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -135,7 +160,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&acc_full[b], 1);
-      tc::mbar_init(&acc_empty[b], 2 * EPI_WARPS);
+      tc::mbar_init(&acc_empty[b], 2 * EW);
     }
     *abort_flag = 0;
     tc::fence_mbar_init();
@@ -156,7 +181,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
       int it = 0;
       const uint32_t bytes = 2u * (A_BYTES + half_n * KS * 2);             // both CTAs' operands of a step
       for (int i = pair; i < count && !*abort_flag; i += pairs) {
-        const Item w = item_at(sh, i);
+        const Item w = plan.item(i);
         const int m0 = w.m * TM + 128 * rank, n0 = w.n * tn + half_n * rank;
         for (int k = w.k0; k < w.k1; ++k, ++it) {
           const int s = it % S;
@@ -189,7 +214,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
       int it = 0, j = 0;
       bool ok = true;
       for (int i = pair; i < count && ok; i += pairs, ++j) {
-        const Item w = item_at(sh, i);
+        const Item w = plan.item(i);
         const int b = j & 1;
         if (*abort_flag || !tc::mbar_wait(&acc_empty[b], ((j >> 1) & 1) ^ 1, check)) { *abort_flag = 1; break; }
         tc::tc_fence_after();
@@ -213,22 +238,23 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
       }
     }
   } else {
-    SlabWriter out{smem + SLAB_OFF + warp * 2 * SLAB, 0};
     const uint32_t acc_empty_even = tc::mapa(&acc_empty[0], 0);
     int j = 0;
     for (int i = pair; i < count; i += pairs, ++j) {
       const int b = j & 1;
+      const Item w = plan.item(i);
+      const int m0 = w.m * TM + 128 * rank, n0 = w.n * tn;
+      epi.ready(w, m0, n0, warp, lane);
       bool have = !*abort_flag && tc::mbar_wait(&acc_full[b], (j >> 1) & 1, check);
       have = __all_sync(0xffffffffu, have);   // tcgen05.ld is warp-collective
       if (!have) { *abort_flag = 1; break; }
       tc::tc_fence_after();
-      const Item w = item_at(sh, i);
-      epi.tile(tc::tmem_addr(tmem, 32 * warp, b * TN), w.m * TM + 128 * rank, w.n * tn, w.part, warp, lane, out);
+      epi.tile(tc::tmem_addr(tmem, 32 * (warp & 3), b * TN), m0, n0, w, warp, lane, smem + SCRATCH_OFF);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_cluster(acc_empty_even + 8 * b);
     }
-    out.drain(lane);
+    epi.done(lane);
   }
 
   tc::tc_fence_before();
@@ -240,6 +266,59 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
     tc::tc_fence_after();
     tc::tmem_dealloc_pair(tmem, TMEM_COLS);
   }
+}
+
+// ----------------------------------------------------------------------------
+// host
+// ----------------------------------------------------------------------------
+
+inline int tiles_of(int64_t v) { return (int)((v + 255) / 256); }
+
+inline Shape shape_of(int64_t M, int64_t N, int64_t K) {
+  Shape s;
+  s.mt = (int)tiles_of(M);
+  s.nt = (int)tiles_of(N);
+  s.ksteps = (int)((K + KS - 1) / KS);
+  s.tn = TN;
+  s.group = s.mt < 16 ? s.mt : 16;
+  s.split_from = s.mt * s.nt;
+  s.split = 1;
+  return s;
+}
+
+// Cut the tiles of the last, partly filled round along K so that every pair has a
+// part.  Worth joining the parts only when it shortens the round by more than a
+// launch takes (about 32 K steps of a quarter of a microsecond).
+inline void split_last_round(Shape& s) {
+  const int pairs = num_sms() / 2, tiles = s.mt * s.nt, rem = tiles % pairs;
+  if (rem == 0) return;
+  int split = pairs / rem;
+  if (split > 8) split = 8;
+  if (split < 2 || s.ksteps - s.ksteps / split < 32) return;
+  s.split_from = tiles - rem;
+  s.split = split;
+}
+
+// One CTA pair per two SMs, or fewer when there are fewer items.
+template <int EW, class Kern, class... Args>
+cudaError_t launch_pairs(Kern kern, int64_t count, cudaStream_t s, const Args&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = num_sms() / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)(count < pairs ? count : pairs), 1, 1);
+  cfg.blockDim = dim3(threads(EW), 1, 1);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace gemm

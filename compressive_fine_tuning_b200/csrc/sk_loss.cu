@@ -74,8 +74,12 @@ struct LogitEpi {
   int T, V, tn;             // tokens of the chunk, classes, classes per tile
   bool store;
   unsigned int* check;
+  gemm::SlabWriter out;
 
-  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, int, int warp, int lane, gemm::SlabWriter& out) {
+  __device__ __forceinline__ void ready(const gemm::Item&, int, int, int, int) {}
+  __device__ __forceinline__ void done(int lane) { out.drain(lane); }
+  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, const gemm::Item&, int warp, int lane,
+                                       uint8_t* scratch) {
     const int t = m0 + 32 * warp + lane;
     if (m0 + 32 * warp >= T) return;
     const int cols = min(tn, V - n0);
@@ -131,7 +135,7 @@ struct LogitEpi {
         }
         sum += part;
       }
-      if (store) out.put(tm_e, e, n0 + 64 * h, m0 + 32 * warp, lane);
+      if (store) out.put(scratch, tm_e, e, n0 + 64 * h, m0 + 32 * warp, warp, lane);
     }
     if (t < T) stats[(int64_t)(n0 / tn) * T + t] = make_float2(m, sum);
   }
@@ -148,12 +152,12 @@ struct LogitArgs {
   unsigned int* check;
 };
 
-__global__ void __launch_bounds__(gemm::THREADS, 1)
+__global__ void __launch_bounds__(gemm::threads(4), 1)
 logit_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_w,
              const __grid_constant__ CUtensorMap tm_e, LogitArgs a) {
   LogitEpi epi{&tm_e, a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.tn,
-               a.store != 0, a.check};
-  gemm::run<0, 0>(&tm_h, &tm_w, a.shape, epi, a.check);
+               a.store != 0, a.check, {}};
+  gemm::run<0, 0, 4>(&tm_h, &tm_w, gemm::Plan{a.shape}, epi, a.check);
 }
 
 // ----------------------------------------------------------------------------
@@ -224,9 +228,13 @@ struct GradEpi {
   const GradOut& o;
   float4* parts;            // [parts][2 CTAs][64 groups of 4 columns][128 rows]
   unsigned int* check;
+  gemm::SlabWriter out;
 
-  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, int part, int warp, int lane,
-                                       gemm::SlabWriter& out) {
+  __device__ __forceinline__ void ready(const gemm::Item&, int, int, int, int) {}
+  __device__ __forceinline__ void done(int lane) { out.drain(lane); }
+  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, const gemm::Item& item, int warp, int lane,
+                                       uint8_t* scratch) {
+    const int part = item.part;
     const int64_t row = m0 + 32 * warp + lane;
     float r = 0.f;
     const uint16_t* wrow = part < 0 && row < o.M ? o.rest.row(row, r, check) : nullptr;
@@ -259,7 +267,7 @@ struct GradEpi {
           for (int e = 0; e < 4; ++e) w[16 * q + 4 * j + e] = f32x2_to_bf16x2(f[2 * e], f[2 * e + 1]);
         }
       }
-      if (part < 0 && (o.acc == nullptr || o.last) && m0 + 32 * warp < o.M) out.put(tm_out, w, c0, m0 + 32 * warp, lane);
+      if (part < 0 && (o.acc == nullptr || o.last) && m0 + 32 * warp < o.M) out.put(scratch, tm_out, w, c0, m0 + 32 * warp, warp, lane);
     }
   }
 };
@@ -273,11 +281,11 @@ struct GradArgs {
 
 // A_MN 0: dH [tokens][d] = P W (P K-major, W MN-major); 1: dW [V][d] = P^T H (both MN-major)
 template <int A_MN>
-__global__ void __launch_bounds__(gemm::THREADS, 1)
+__global__ void __launch_bounds__(gemm::threads(4), 1)
 grad_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
             const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ GradArgs a) {
-  GradEpi epi{&tm_out, a.out, a.parts, a.check};
-  gemm::run<A_MN, 1>(&tm_a, &tm_b, a.shape, epi, a.check);
+  GradEpi epi{&tm_out, a.out, a.parts, a.check, {}};
+  gemm::run<A_MN, 1, 4>(&tm_a, &tm_b, gemm::Plan{a.shape}, epi, a.check);
 }
 
 // Joins the parts of the tiles that were cut along K, in part order: block
@@ -469,8 +477,6 @@ __global__ void __launch_bounds__(256) scale_kernel(uint4* __restrict__ x, int64
 // workspace and launches
 // ----------------------------------------------------------------------------
 
-int64_t tiles_of(int64_t v) { return (v + 255) / 256; }
-
 // Tokens per chunk.  With gradients: the largest multiple of 256 whose rows of
 // exponentials fit the buffer (256 at least).
 int64_t chunk_tokens(int64_t T, int64_t V, bool grads) {
@@ -515,40 +521,6 @@ cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t col
                       (uint32_t)box_cols, (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <class Kern, class Args>
-cudaError_t launch_pairs(Kern kern, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const Args& args,
-                         cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm::SMEM);
-  if (e != cudaSuccess) return e;
-  const int tiles = gemm::items(args.shape), pairs = num_sms() / 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * (unsigned)(tiles < pairs ? tiles : pairs), 1, 1);
-  cfg.blockDim = dim3(gemm::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = gemm::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, args);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-gemm::Shape shape_of(int64_t M, int64_t N, int64_t K) {
-  gemm::Shape s;
-  s.mt = (int)tiles_of(M);
-  s.nt = (int)tiles_of(N);
-  s.ksteps = (int)((K + gemm::KS - 1) / gemm::KS);
-  s.tn = gemm::TN;
-  s.group = s.mt < 16 ? s.mt : 16;
-  s.split_from = s.mt * s.nt;
-  s.split = 1;
-  return s;
-}
-
 // The loss alone: classes per tile.  The pairs take the tiles in rounds, and few
 // tokens make few tiles, so a tile is narrowed until the last round is as full as
 // the others (the time goes with rounds * width).
@@ -564,20 +536,6 @@ void balance_tiles(gemm::Shape& s, int64_t V) {
     }
   }
   s.split_from = s.mt * s.nt;
-}
-
-// A gradient product: cut the tiles of the last, partly filled round along K so
-// that every pair has a part.  Worth a second launch that joins the parts only
-// when it shortens the round by more than that launch takes (about 32 K steps of
-// a quarter of a microsecond).
-void split_last_round(gemm::Shape& s) {
-  const int pairs = num_sms() / 2, tiles = s.mt * s.nt, rem = tiles % pairs;
-  if (rem == 0) return;
-  int split = pairs / rem;
-  if (split > 8) split = 8;
-  if (split < 2 || s.ksteps - s.ksteps / split < 32) return;
-  s.split_from = tiles - rem;
-  s.split = split;
 }
 
 cudaError_t launch_join(const GradArgs& a, uint16_t* out, cudaStream_t s) {
@@ -628,13 +586,13 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     SK_TRY(map_rows(&tm_h, H, T, a.d, a.d, 64, 128));
     tm_e = tm_h;                                   // not used without gradients
     if (grads) SK_TRY(map_rows(&tm_e, E, T, a.V, l.pitch, 64, 32));
-    gemm::Shape shape = shape_of(T, a.V, a.d);
+    gemm::Shape shape = gemm::shape_of(T, a.V, a.d);
     if (!grads) balance_tiles(shape, a.V);
     CUtensorMap tm_w;
     SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, shape.tn / 2));
     LogitArgs la{shape, stats, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
                  grads ? 1 : 0, a.check};
-    SK_TRY(launch_pairs(logit_kernel, tm_h, tm_w, tm_e, la, s));
+    SK_TRY(gemm::launch_pairs<4>(logit_kernel, gemm::items(la.shape), s, tm_h, tm_w, tm_e, la));
     lse_kernel<<<(unsigned)((T + 7) / 8), dim3(8, 32), 0, s>>>(stats, nll, target, a.target64, a.ignore_index,
                                                                  (int)T, a.V, shape.nt, lse, losses ? losses + t0 : nullptr,
                                                                  a.check);
@@ -649,19 +607,19 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
       CUtensorMap tm_p, tm_dh;
       SK_TRY(map_rows(&tm_p, E, T, a.V, l.pitch, 64, 128));
       SK_TRY(map_rows(&tm_dh, a.dH + t0 * a.d, T, a.d, a.d, 64, 32));
-      GradArgs ga{shape_of(T, a.d, a.V),
+      GradArgs ga{gemm::shape_of(T, a.d, a.V),
                   {nullptr, 0, 1, T, a.d, {rest, a.W, target, a.target64, a.V, a.d, a.ignore_index}}, parts, a.check};
-      split_last_round(ga.shape);
-      SK_TRY(launch_pairs(grad_kernel<0>, tm_p, tm_w_mn, tm_dh, ga, s));
+      gemm::split_last_round(ga.shape);
+      SK_TRY(gemm::launch_pairs<4>(grad_kernel<0>, gemm::items(ga.shape), s, tm_p, tm_w_mn, tm_dh, ga));
       SK_TRY(launch_join(ga, a.dH + t0 * a.d, s));
     }
     if (dw) {
       CUtensorMap tm_p, tm_hm;
       SK_TRY(map_rows(&tm_p, E, T, a.V, l.pitch, 64, 64));
       SK_TRY(map_rows(&tm_hm, H, T, a.d, a.d, 64, 64));
-      GradArgs ga{shape_of(a.V, a.d, T), {acc, t0 > 0 ? 1 : 0, t0 + T >= a.T ? 1 : 0, a.V, a.d, {}}, parts, a.check};
-      split_last_round(ga.shape);
-      SK_TRY(launch_pairs(grad_kernel<1>, tm_p, tm_hm, tm_dw, ga, s));
+      GradArgs ga{gemm::shape_of(a.V, a.d, T), {acc, t0 > 0 ? 1 : 0, t0 + T >= a.T ? 1 : 0, a.V, a.d, {}}, parts, a.check};
+      gemm::split_last_round(ga.shape);
+      SK_TRY(gemm::launch_pairs<4>(grad_kernel<1>, gemm::items(ga.shape), s, tm_p, tm_hm, tm_dw, ga));
       SK_TRY(launch_join(ga, a.dW, s));
     }
   }

@@ -6,335 +6,261 @@
 // i.e. the corrected Eq. 6 of the "Sketch to Adapt" OpenReview discussion (reply
 // Q1) with X as the checkpoint holds it (format in sk_ckpt8.cuh).
 //
-// Tensor cores: the G tile [256 rows i x 256 columns j] = dY^T X over K = tokens
-// on a CTA pair, binned by the epilogue into (group, centroid) sums that never
-// leave the SM as a dense gradient.  dY comes by TMA.  X is dequantised on its
-// way into shared memory: a warp owns eight tokens of every 64-token step, a
-// lane one token's 32-column block, i.e. 32 bytes and one scale byte, loaded a
-// step ahead, so the checkpoint is read at 33/64 of the bytes of a bf16 X and no
-// bf16 copy of it ever exists in memory.  q * 2^e is exact in bf16, so the
-// products are those of the stored values, accumulated in fp32.
-// The bound is the tensor pipe (2 T n d flops).
+// Tensor cores: a pass over the checkpoint writes the layer's X as bf16 (exact) to
+// the workspace, in task order when there are several LUT sets, and the
+// persistent product of sk_gemm.cuh forms the G tiles [256 rows i x 256 columns j]
+// = dY^T X over K = the set's tokens, both operands MN-major.  G is never written:
+// while the next tile's MMAs run, the epilogue adds a finished tile's columns into
+// the (group, centroid) bins of its rows and writes the bins.  The bound is the
+// tensor pipe (2 T n d flops) from about 500 tokens per set on, the binning of
+// n d accumulators per set below.
+//
+// The pass costs 33/32 + 2 bytes per value, 18 us next to a product of about 500
+// at [8192, 4096] x [8192, 11008].  Dequantising in the product instead (warps
+// that write the operand tiles in place of the copy engine) was built first and
+// ran at 726 us: every step of every pair then waits for sixteen warps of two SMs,
+// and each of the 43 row blocks dequantises X again.
+#include <type_traits>
+
+#include "sk_gemm.cuh"
 #include "sk_lut8.cuh"
-#include "sk_tc.cuh"
 
 namespace sk {
 namespace {
 
-constexpr int KS = 64;                 // tokens per pipeline step
-constexpr int N = 256;                 // columns per tile
-constexpr int A_BYTES = 2 * 8192;      // this CTA's 128 rows of dY^T: two 64-row MN atoms
-constexpr int B_BYTES = 2 * 8192;      // this CTA's 128 columns of X: two 64-column MN atoms
-constexpr int STAGE = A_BYTES + B_BYTES;
-constexpr int S = 3;                   // two CTAs per SM: one bins while the other multiplies
-constexpr int BAR_OFF = S * STAGE;
-constexpr int SMEM = 1024 + BAR_OFF + 256;
-constexpr int PRODUCERS = 8, TMA_WARP = 8, MMA_WARP = 9, THREADS = 320;
-constexpr uint32_t IDESC = tc::idesc_bf16(256, N, 1, 1);
-constexpr int TMEM_COLS = 256;
-constexpr int COPIES = 4;             // copies of the bins in the epilogue
-static_assert(PRODUCERS * 8 == KS, "a producer warp fills one K-group of eight tokens");
+using gemm::KS;
+using gemm::TN;
 
-__host__ __device__ constexpr int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+constexpr int COPIES = 2;              // copies of the bins per epilogue thread
+static_assert(COPIES * 16 * 256 * 4 <= gemm::SCRATCH, "the bins fit the epilogue's shared memory");
 
 // Group slots of one 256-column tile.
 __host__ __device__ inline int group_slots(int64_t gs, int gpr) {
-  const int64_t s = 255 / gs + 2;
+  const int64_t s = (TN - 1) / gs + 2;
   return (int)(s < gpr ? s : gpr);
 }
 
 struct Lut8Args {
+  gemm::Shape shape;         // of one LUT set
   const uint8_t* packed;
   int64_t row_bytes;
-  const int8_t* q;
-  const uint8_t* scale;
-  int64_t n, d, gs, T;
-  int gpr, slots;
+  int64_t n, d, gs;
+  int gpr, slots, sets;
   float* part;               // [sets][jtiles][n][slots][k] partial bins
   int64_t part_set_stride;
-  unsigned int* check;
-  // several LUT sets: dY rows in task order, set z's tokens at positions
-  // [segs[2z], segs[2z] + segs[2z + 1]) (64-aligned, zero rows between), perm
-  // maps a position to its token; nullptr for one LUT set
+  float* extra;              // [cut parts beyond a tile's first][256][slots][k]
+  // several LUT sets: rows in task order, set z's tokens at positions
+  // [segs[2z], segs[2z] + segs[2z + 1]) (multiples of 64 apart, zero rows between);
+  // nullptr for one LUT set
   const int* segs;
-  const int* perm;
-  int row_pairs;
+  unsigned int* check;
 };
 
-template <int BITS, bool ROUTED>
-__global__ void __launch_bounds__(THREADS, 2) lut8_tc_kernel(const __grid_constant__ CUtensorMap tm_dy, Lut8Args a) {
-  constexpr int K = 1 << BITS;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + BAR_OFF);  // even CTA: both CTAs' dY landed
-  uint64_t* full_b = full_a + S;                                    // even CTA: both CTAs' X tiles written
-  uint64_t* empty = full_b + S;                                     // both CTAs: the pair MMAs read the stage
-  uint64_t* d_full = empty + S;                                     // both CTAs: accumulator final
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_full + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
-  const int warp = tc::warp_id(), lane = tc::lane_id();
-  const uint32_t rank = tc::cluster_ctarank();                      // 0: issues the MMAs
-  // grid: (pair, column tile, row block + row_pairs * LUT set), column tiles fastest after the pair
-  const int jt = blockIdx.y;
-  const int64_t j0 = (int64_t)jt * N;
-  const int set = (int)blockIdx.z / a.row_pairs;
-  const int64_t i0 = (int64_t)((int)blockIdx.z - set * a.row_pairs) * 256 + 128 * rank;
-  int k_first = 0;
-  int tokens = (int)a.T;
-  if constexpr (ROUTED) {
-    k_first = a.segs[2 * set];
-    tokens = a.segs[2 * set + 1];
+// items: set after set, each set's tiles in the product's order
+struct Lut8Plan {
+  const Lut8Args& a;
+  __device__ __forceinline__ int count() const {
+    return a.segs == nullptr ? gemm::items(a.shape) : a.sets * a.shape.mt * a.shape.nt;
   }
-  const int nsteps = ceil_div(tokens, KS);      // a set with no tokens writes zero partials
-  float* part = a.part + (int64_t)set * a.part_set_stride;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      tc::mbar_init(&full_a[s], 1);
-      tc::mbar_init(&full_b[s], 2 * PRODUCERS);
-      tc::mbar_init(&empty[s], 1);
-    }
-    tc::mbar_init(d_full, 1);
-    *abort_flag = 0;
-    tc::fence_mbar_init();
+  __device__ __forceinline__ int tn() const { return TN; }
+  __device__ __forceinline__ int set_of(int i) const { return a.segs == nullptr ? 0 : i / (a.shape.mt * a.shape.nt); }
+  __device__ __forceinline__ gemm::Item item(int i) const {
+    if (a.segs == nullptr) return gemm::item_at(a.shape, i);
+    const int set = set_of(i);
+    gemm::Item it;
+    gemm::tile_at(a.shape, i - set * a.shape.mt * a.shape.nt, it.m, it.n);
+    it.part = set;                                     // a whole tile of this set
+    it.k0 = __ldg(a.segs + 2 * set) / KS;
+    it.k1 = it.k0 + (__ldg(a.segs + 2 * set + 1) + KS - 1) / KS;
+    return it;
   }
-  if (warp == MMA_WARP) tc::tmem_alloc_pair(tmem_slot, TMEM_COLS);
-  if (warp == TMA_WARP && lane == 0) tc::tma_prefetch(&tm_dy);
-  tc::tc_fence_before();
-  // both CTAs' barriers are initialised before either CTA signals the other
-  tc::cluster_sync_all();
-  tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+};
 
-  if (warp == TMA_WARP) {
-    if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < nsteps && !*abort_flag; ++i) {
-        const int s = i % S;
-        if (!tc::mbar_wait(&empty[s], ((i / S) & 1) ^ 1, a.check)) { *abort_flag = 1; break; }
-        uint8_t* st = smem + s * STAGE;
-        if (rank == 0) tc::mbar_arrive_expect_tx(&full_a[s], 2 * A_BYTES);   // the bytes of both CTAs
-        const uint32_t bar = tc::mapa(&full_a[s], 0);
-        const int tk = k_first + i * KS;
-        tc::tma_load_2d_pair(st, &tm_dy, bar, (int)i0, tk);
-        tc::tma_load_2d_pair(st + 8192, &tm_dy, bar, (int)i0 + 64, tk);
-        ++issued;
-      }
-      // never leave with a copy still landing in shared memory: the pair MMAs
-      // read every landed stage before they free it
-      bool ok = true;
-      for (int k = issued > S ? issued - S : 0; k < issued && ok; ++k)
-        ok = tc::mbar_wait(&empty[k % S], (k / S) & 1, a.check);
-    }
-  } else if (warp == MMA_WARP) {
-    if (rank == 0 && lane == 0) {
-      bool ok = true;
-      for (int i = 0; i < nsteps; ++i) {
-        const int s = i % S;
-        if (*abort_flag || !tc::mbar_wait(&full_a[s], (i / S) & 1, a.check) ||
-            !tc::mbar_wait(&full_b[s], (i / S) & 1, a.check)) {
-          *abort_flag = 1; ok = false; break;
-        }
-        tc::tc_fence_after();
-        const uint32_t ab = tc::smem_u32(smem + s * STAGE), bb = ab + A_BYTES;
-#pragma unroll
-        for (int kk = 0; kk < KS / 16; ++kk) {
-          const uint64_t ad = tc::sdesc(ab + kk * 2048, 8192, 1024, tc::kSwizzle128);
-          const uint64_t bd = tc::sdesc(bb + kk * 2048, 8192, 1024, tc::kSwizzle128);
-          tc::mma_ss_pair(tmem, ad, bd, IDESC, (i > 0 || kk > 0) ? 1u : 0u);
-        }
-        tc::mma_commit_pair(&empty[s]);
-      }
-      if (ok) tc::mma_commit_pair(d_full);
-    }
-  } else {
-    // producers: lane (r8, h) of warp w dequantises token 8 w + r8 of the step,
-    // columns 32 h .. 32 h + 31 of this CTA's 128
-    const int r8 = lane & 7, h = lane >> 3;
-    const int lr = 8 * warp + r8;
-    // the epilogue warps' row indices of this column tile, loaded while the MMAs
-    // run so that their memory latency is off the binning loop
-    const int64_t row_i = i0 + threadIdx.x;
-    Chunk<BITS> chunks[N / 32] = {};
-    if (warp < 4 && row_i < a.n) {
-#pragma unroll
-      for (int b = 0; b < N / 32; ++b)
-        if (j0 + 32 * b < a.d) chunks[b] = load_chunk<BITS>(a.packed + row_i * a.row_bytes, (j0 >> 5) + b);
-    }
-    const int64_t j = j0 + 128 * rank + 32 * h;
-    const bool col_ok = j < a.d;
-    const int64_t sblocks = a.d >> 5;
-    uint32_t slot_off[4];              // 16-byte swizzled slots of the block's four bf16 quarters
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      slot_off[e] = (h >> 1) * 8192 + warp * 1024 + r8 * 128 + (((4 * (h & 1) + e) ^ r8) << 4);
-    // 32 bytes and a scale byte per step, loaded two steps ahead; a position's
-    // token (one LUT set: the position itself) is known one step before that
-    const int8_t* q_col = a.q + j;
-    const uint8_t* s_col = a.scale + (j >> 5);
-    auto token_of = [&](int i) -> int {
-      const int t = i * KS + lr;
-      if (t >= tokens || !col_ok) return -1;
-      return ROUTED ? __ldg(a.perm + k_first + t) : t;
-    };
-    struct Block {
-      uint4 q0, q1;
-      uint32_t byte;
-    };
-    auto fetch = [&](int t) -> Block {
-      Block b{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u), 0u};   // zero scale: the tile's padding is zero
-      if (t >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(q_col + (int64_t)t * a.d);
-        b.q0 = __ldg(src);
-        b.q1 = __ldg(src + 1);
-        b.byte = __ldg(s_col + (int64_t)t * sblocks);
-      }
-      return b;
-    };
-    Block ahead[2] = {fetch(token_of(0)), fetch(token_of(1))};
-    int tok = token_of(2);
-    const uint32_t full_b_even = tc::mapa(&full_b[0], 0);
-    bool ok = true;
-#pragma unroll 1
-    for (int i0s = 0; i0s < nsteps && ok; i0s += 2) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int i = i0s + half;
-        if (i >= nsteps || !ok) break;
-        const Block cur = ahead[half];
-        ahead[half] = fetch(tok);
-        tok = token_of(i + 3);
-        const uint32_t s2 = ckpt8_scale2(cur.byte);
-        uint4 o[4];
-        ckpt8_dequant4(cur.q0.x, s2, o[0].x, o[0].y);
-        ckpt8_dequant4(cur.q0.y, s2, o[0].z, o[0].w);
-        ckpt8_dequant4(cur.q0.z, s2, o[1].x, o[1].y);
-        ckpt8_dequant4(cur.q0.w, s2, o[1].z, o[1].w);
-        ckpt8_dequant4(cur.q1.x, s2, o[2].x, o[2].y);
-        ckpt8_dequant4(cur.q1.y, s2, o[2].z, o[2].w);
-        ckpt8_dequant4(cur.q1.z, s2, o[3].x, o[3].y);
-        ckpt8_dequant4(cur.q1.w, s2, o[3].z, o[3].w);
-        const int s = i % S;
-        if (*abort_flag || !tc::mbar_wait(&empty[s], ((i / S) & 1) ^ 1, a.check)) { *abort_flag = 1; ok = false; break; }
-        uint8_t* bt = smem + s * STAGE + A_BYTES;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(bt + slot_off[e]) = o[e];
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(full_b_even + 8 * s);
-      }
-    }
-    if (warp < 4) {
-      // epilogue: thread = row i (TMEM lane); bin the row's 256 columns
-      __syncwarp();
-      // [COPIES][K][128], tail of stage memory: consecutive columns add into different
-      // copies, so their loads do not wait for one another's stores
-      float* bins = reinterpret_cast<float*>(smem + BAR_OFF - COPIES * K * 128 * 4) + threadIdx.x;
-      bool have = !*abort_flag && tc::mbar_wait(d_full, 0, a.check) && nsteps > 0;   // no steps: nothing accumulated
-      have = __all_sync(0xffffffffu, have);  // tcgen05.ld is warp-collective
-      if (have) tc::tc_fence_after();
-      // the bins reuse the last stages' memory: every MMA has read it (d_full)
-#pragma unroll
-      for (int c = 0; c < COPIES * K; ++c) bins[c * 128] = 0.f;
-      const int first_g = (int)(j0 / a.gs);
-      const int gs32 = (int)a.gs;
-      int g = first_g, g_end = (first_g + 1) * gs32;
-      bool dirty = false;
-      auto flush = [&](int gg) {
-        float4* dst = reinterpret_cast<float4*>(part + (((int64_t)jt * a.n + row_i) * a.slots + (gg - first_g)) * K);
-#pragma unroll
-        for (int c4 = 0; c4 < K / 4; ++c4) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = 4 * c4 + e;
-            v[e] = bins[c * 128];
-            bins[c * 128] = 0.f;
-#pragma unroll
-            for (int k = 1; k < COPIES; ++k) {
-              v[e] += bins[(k * K + c) * 128];
-              bins[(k * K + c) * 128] = 0.f;
-            }
-          }
-          if (row_i < a.n) dst[c4] = make_float4(v[0], v[1], v[2], v[3]);
-        }
-      };
-#pragma unroll
-      for (int b = 0; b < N / 32; ++b) {
-        const int64_t jc = j0 + 32 * b;
-        if (jc >= a.d) break;
-        uint32_t v[32];
-        if (have) {
-          tc::tmem_ld32(tc::tmem_addr(tmem, warp * 32, 32 * b), v);
-          tc::tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0u;
-        }
-        if ((int)jc >= g_end) {       // chunk in a later group: hand the finished group's sums on
-          if (dirty) flush(g);
-          do { ++g; g_end += gs32; } while ((int)jc >= g_end);
-          dirty = false;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += COPIES) {
-          float* at[COPIES];
-          float sum[COPIES];
-#pragma unroll
-          for (int k = 0; k < COPIES; ++k) {
-            at[k] = bins + (k * K + chunk_index<BITS>(chunks[b], e + k)) * 128;
-            sum[k] = *at[k];
-          }
-#pragma unroll
-          for (int k = 0; k < COPIES; ++k) *at[k] = sum[k] + __uint_as_float(v[e + k]);
-        }
-        dirty = true;
-      }
-      if (dirty) flush(g);
-    }
-  }
+// shared memory by its 32-bit address plus a constant (through a pointer that has
+// lost its address space every access would be a generic one)
+template <int OFF>
+__device__ __forceinline__ float lds(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1 + %2];" : "=f"(v) : "r"(a), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ void sts(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0 + %1], %2;" ::"r"(a), "n"(OFF), "f"(v));
+}
 
-  tc::tc_fence_before();
-  __syncthreads();
-  // neither CTA leaves (or frees tensor memory) while the other may still
-  // signal its barriers or the pair MMAs may still use its memory
-  tc::cluster_sync_all();
-  if (warp == MMA_WARP) {
-    tc::tc_fence_after();
-    tc::tmem_dealloc_pair(tmem, TMEM_COLS);
+// index e of a chunk times 1024
+template <int BITS>
+__device__ __forceinline__ uint32_t index_1024(const Chunk<BITS>& ch, int e) {
+  if constexpr (BITS == 3) return chunk_index<3>(ch, e) << 10;
+  const int bit = e * BITS, s = bit & 31;
+  const uint32_t w = ch.w[bit >> 5], mask = ((1u << BITS) - 1u) << 10;
+  return (s >= 10 ? w >> (s - 10) : w << (10 - s)) & mask;
+}
+
+template <int N, class F>
+__device__ __forceinline__ void unroll(F f) {
+  if constexpr (N > 0) {
+    unroll<N - 1>(f);
+    f(std::integral_constant<int, N - 1>());
   }
 }
 
-// Sum the partial bins of every (set, row, group) over the column tiles that
-// touch the group, in tile order, and write (or add to) dlut: four bins a thread.
+// Bins the accumulator's columns.  Eight warps: thread = (row, half of the tile's
+// columns), so that two warps of a scheduler fill each other's waits.  A thread's
+// bins are its own column of shared memory, [COPIES][K][256 threads], and
+// consecutive columns add into different copies.  The group that spans the
+// halves' border is written by the lower half with both halves' sums.
 template <int BITS>
-__global__ void __launch_bounds__(256) lut8_reduce_kernel(const float4* __restrict__ part, int64_t n, int gpr, int64_t gs,
-                                                          int jtiles, int slots, float4* __restrict__ dlut,
-                                                          int accumulate, int64_t total, int64_t part_set_stride) {
+struct BinEpi {
+  static constexpr int K = 1 << BITS, HB = TN / 64;
+  static constexpr int COPY = K * 1024;              // bytes between a thread's copies
+  const Lut8Args& a;
+  Chunk<BITS> chunks[HB];            // the row's indices of this half tile
+
+  __device__ __forceinline__ void ready(const gemm::Item&, int m0, int n0, int warp, int lane) {
+    const int64_t row = m0 + 32 * (warp & 3) + lane;
+    const int64_t c0 = n0 + 128 * (warp >> 2);
+    if (row >= a.n) return;
+    const uint8_t* src = a.packed + row * a.row_bytes;
+#pragma unroll
+    for (int b = 0; b < HB; ++b)
+      if (c0 + 32 * b < a.d) chunks[b] = load_chunk<BITS>(src, (c0 >> 5) + b);
+  }
+  __device__ __forceinline__ void done(int) {}
+
+  // The sums of a group: out, and the bins to zero.  `both`: the other half's too
+  // (512 bytes further on; it zeroes its own).
+  __device__ __forceinline__ void flush(uint32_t bins, float4* out, bool write, bool both) {
+#pragma unroll 1
+    for (int c4 = 0; c4 < K / 4; ++c4, bins += 4096, ++out) {
+      float v[4];
+      unroll<4>([&](auto e) {
+        v[e] = lds<e * 1024>(bins) + lds<e * 1024 + COPY>(bins);
+        sts<e * 1024>(bins, 0.f);
+        sts<e * 1024 + COPY>(bins, 0.f);
+      });
+      if (both) unroll<4>([&](auto e) { v[e] += lds<e * 1024 + 512>(bins) + lds<e * 1024 + 512 + COPY>(bins); });
+      if (write) *out = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  __device__ __forceinline__ void clear(uint32_t bins) {
+    unroll<COPIES * K>([&](auto c) { sts<c * 1024>(bins, 0.f); });
+  }
+
+  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, const gemm::Item& it, int warp, int lane,
+                                       uint8_t* scratch) {
+    const int quad = warp & 3, half = warp >> 2;
+    const int64_t row = m0 + 32 * quad + lane;
+    const bool have = it.k1 > it.k0;                   // a set without tokens: zeros
+    const uint32_t bins = tc::smem_u32(scratch) + 4 * (128 * half + 32 * quad + lane);
+    clear(bins);
+    // where this tile's partial bins go
+    float* dst;
+    if (a.segs == nullptr && it.part >= 0 && it.part % a.shape.split != 0) {
+      const int q = it.part % a.shape.split, cut = it.part / a.shape.split;
+      dst = a.extra + (((int64_t)cut * (a.shape.split - 1) + q - 1) * gemm::TM + (row - (int64_t)it.m * gemm::TM)) * a.slots * K;
+    } else {
+      const int64_t set = a.segs == nullptr ? 0 : it.part;
+      dst = a.part + set * a.part_set_stride + ((int64_t)it.n * a.n + row) * a.slots * K;
+    }
+    const int gs = (int)a.gs, first_g = n0 / gs;
+    const int c0 = n0 + 128 * half;
+    const int nb = a.d <= c0 ? 0 : a.d - c0 < 128 ? (int)(a.d - c0) / 32 : HB;     // chunks of this half
+    // a group on both sides of the border: the two warps of these rows meet when
+    // each has all of its share, and again when the lower one has read the upper's
+    const int border = n0 + 128;
+    const bool shared_g = border < a.d && border % gs != 0;
+    auto meet = [&] { tc::named_bar_sync(1 + quad, 64); };
+    int g = c0 / gs, g_end = (g + 1) * gs;
+    bool waiting = half == 1 && shared_g;              // this half's first group belongs to the lower one
+    auto finish = [&](bool last) {
+      if (waiting) {
+        meet();
+        meet();
+        clear(bins);
+        waiting = false;
+      } else {
+        const bool both = last && half == 0 && shared_g;
+        if (both) meet();
+        flush(bins, reinterpret_cast<float4*>(dst + (g - first_g) * K), row < a.n, both);
+        if (both) meet();
+      }
+    };
+    // one copy of the code for all chunks: instruction fetches count here
+    // (unrolled over the chunks: 8 % slower)
+#pragma unroll 1
+    for (int b = 0; b <= nb; ++b) {
+      const int jc = c0 + 32 * b;
+      if (b == nb) {
+        if (nb > 0) finish(true);
+        break;
+      }
+      if (jc >= g_end) {               // a later group (d / gpr is a multiple of 32): hand the finished one on
+        finish(false);
+        do { ++g; g_end += gs; } while (jc >= g_end);
+      }
+      const Chunk<BITS> ch = chunks[0];
+#pragma unroll
+      for (int q = 0; q + 1 < HB; ++q) chunks[q] = chunks[q + 1];
+      uint32_t v[32];
+      if (have) {
+        tc::tmem_ld32(tmem + 128 * half + 32 * b, v);
+        tc::tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0u;
+      }
+      unroll<16>([&](auto e2) {
+        const uint32_t at0 = bins + index_1024<BITS>(ch, 2 * e2), at1 = bins + index_1024<BITS>(ch, 2 * e2 + 1);
+        const float s0 = lds<0>(at0), s1 = lds<COPY>(at1);
+        sts<0>(at0, s0 + __uint_as_float(v[2 * e2]));
+        sts<COPY>(at1, s1 + __uint_as_float(v[2 * e2 + 1]));
+      });
+    }
+  }
+};
+
+template <int BITS>
+__global__ void __launch_bounds__(gemm::threads(8), 1)
+lut8_tc_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x,
+               const __grid_constant__ Lut8Args a) {
+  BinEpi<BITS> epi{a, {}};
+  gemm::run<1, 1, 8>(&tm_dy, &tm_x, Lut8Plan{a}, epi, a.check);
+}
+
+// Sum the partial bins of every (set, row, group) over the column tiles that
+// touch the group, in tile order (a tile's cut parts in part order), and write (or
+// add to) dlut: four bins a thread.
+template <int BITS, bool CUT>
+__global__ void __launch_bounds__(256) lut8_reduce_kernel(const __grid_constant__ Lut8Args a, float4* __restrict__ dlut,
+                                                          int accumulate, int64_t total) {
   constexpr int Q = (1 << BITS) / 4;
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (e >= total) return;
   const int c = (int)(e % Q);
   const int64_t ig = e / Q;
-  const int g = (int)(ig % gpr);
-  const int64_t si = ig / gpr, set = si / n, i = si - set * n;
-  part += set * part_set_stride;
-  const int t_first = (int)(((int64_t)g * gs) / N);
-  int t_last = (int)(((int64_t)(g + 1) * gs - 1) / N);
-  if (t_last > jtiles - 1) t_last = jtiles - 1;
+  const int g = (int)(ig % a.gpr);
+  const int64_t si = ig / a.gpr, set = si / a.n, i = si - set * a.n;
+  const float4* part = reinterpret_cast<const float4*>(a.part + set * a.part_set_stride);
+  const float4* extra = reinterpret_cast<const float4*>(a.extra);
+  const int t_first = (int)(((int64_t)g * a.gs) / TN);
+  const int t_last = (int)(((int64_t)(g + 1) * a.gs - 1) / TN);
+  const int m = (int)(i / gemm::TM);
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& v) { sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w); };
 #pragma unroll 4
   for (int t = t_first; t <= t_last; ++t) {
     // only a group's first tile can start in an earlier group
-    const int slot = t == t_first ? g - (int)(((int64_t)t * N) / gs) : 0;
-    const float4 v = __ldg(part + (((int64_t)t * n + i) * slots + slot) * Q + c);
-    sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+    const int slot = t == t_first ? g - (int)(((int64_t)t * TN) / a.gs) : 0;
+    add(__ldg(part + (((int64_t)t * a.n + i) * a.slots + slot) * Q + c));
+    if constexpr (CUT) {
+      const int cut = gemm::tile_index(a.shape, m, t) - a.shape.split_from;
+      for (int q = 0; cut >= 0 && q < a.shape.split - 1; ++q)
+        add(__ldg(extra + ((((int64_t)cut * (a.shape.split - 1) + q) * gemm::TM + (i - (int64_t)m * gemm::TM)) * a.slots + slot) * Q + c));
+    }
   }
-  if (accumulate) {
-    const float4 o = dlut[e];
-    sum = make_float4(o.x + sum.x, o.y + sum.y, o.z + sum.z, o.w + sum.w);
-  }
+  if (accumulate) add(dlut[e]);
   dlut[e] = sum;
 }
 
@@ -399,20 +325,66 @@ __global__ void __launch_bounds__(kRouteThreads) lut8_route_kernel(const int32_t
   }
 }
 
-__global__ void lut8_gather_kernel(const uint4* __restrict__ src, const int* __restrict__ perm, int positions,
-                                   int64_t units, uint4* __restrict__ dst) {
-  const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (e >= (int64_t)positions * units) return;
-  const int64_t p = e / units, u = e - p * units;
+// dY rows in task order, zero rows between the segments.
+__global__ void __launch_bounds__(256) lut8_gather_kernel(const uint4* __restrict__ src, const int* __restrict__ perm,
+                                                          int64_t units, uint4* __restrict__ dst) {
+  const int64_t p = blockIdx.y;
   const int t = perm[p];
-  dst[e] = t >= 0 ? __ldg(src + (int64_t)t * units + u) : make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256)
+    dst[p * units + u] = t >= 0 ? __ldg(src + (int64_t)t * units + u) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-int route_positions(int64_t T, int ntask) { return (int)(T + (int64_t)ntask * (KS - 1)); }
+// The checkpoint's rows as bf16 in task order, zero rows between the segments.
+__global__ void __launch_bounds__(256) lut8_dequant_rows_kernel(const uint2* __restrict__ q,
+                                                                const uint8_t* __restrict__ scale,
+                                                                const int* __restrict__ perm, int64_t units,
+                                                                uint4* __restrict__ X) {
+  const int64_t p = blockIdx.y;
+  const int t = perm[p];
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
+    uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    if (t >= 0) {
+      const int64_t at = (int64_t)t * units + u;
+      const uint2 v = __ldg(q + at);
+      const uint32_t s2 = ckpt8_scale2(__ldg(scale + (at >> 2)));
+      ckpt8_dequant4(v.x, s2, o.x, o.y);
+      ckpt8_dequant4(v.y, s2, o.z, o.w);
+    }
+    X[p * units + u] = o;
+  }
+}
 
-size_t route_bytes(int64_t n, int64_t T, int ntask) {
-  const int64_t pos = route_positions(T, ntask);
-  return ((size_t)(pos + 2 * ntask) * 4 + 255) / 256 * 256 + ((size_t)pos * n * 2 + 255) / 256 * 256;
+int64_t route_positions(int64_t T, int ntask) { return T + (int64_t)ntask * (KS - 1); }
+
+size_t pad256(size_t b) { return (b + 255) / 256 * 256; }
+
+struct Layout {
+  size_t perm, segs, dy, x, part, extra, total;
+  int64_t rows;
+};
+
+size_t part_floats(int64_t n, int64_t d, int bits, int gpr) {
+  return (size_t)gemm::tiles_of(d) * n * group_slots(d / gpr, gpr) * (1 << bits);
+}
+
+Layout layout(int64_t n, int64_t d, int bits, int gpr, int64_t T, int ntask, bool routed) {
+  Layout l;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += pad256(bytes);
+    return here;
+  };
+  l.rows = routed ? route_positions(T, ntask) : T;
+  l.perm = take(routed ? (size_t)l.rows * 4 : 0);
+  l.segs = take(routed ? (size_t)ntask * 8 : 0);
+  l.dy = take(routed ? (size_t)l.rows * n * 2 : 0);
+  l.x = take((size_t)l.rows * d * 2);
+  l.part = take((routed ? ntask : 1) * part_floats(n, d, bits, gpr) * 4);
+  // at most one part per CTA pair in the cut round
+  l.extra = take(routed ? 0 : (size_t)(num_sms() / 2) * gemm::TM * group_slots(d / gpr, gpr) * (1 << bits) * 4);
+  l.total = at;
+  return l;
 }
 
 // ----------------------------------------------------------------------------
@@ -482,87 +454,84 @@ __global__ void __launch_bounds__(kBlock) lut8_simt_kernel(Problem p, const int8
   }
 }
 
-size_t part_floats(int64_t n, int64_t d, int bits, int gpr) {
-  return (size_t)ceil_div(d, N) * n * group_slots(d / gpr, gpr) * (1 << bits);
-}
-
 }  // namespace
 
 size_t lut8_tc_workspace(int64_t n, int64_t d, int bits, int gpr, int64_t T, int ntask, bool routed) {
-  const size_t part = part_floats(n, d, bits, gpr) * sizeof(float);
-  return routed ? route_bytes(n, T, ntask) + (size_t)ntask * part : part;
+  return layout(n, d, bits, gpr, T, ntask, routed).total;
 }
 
 cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* scale, const uint16_t* dY, float* dlut,
                            int accumulate, bool routed, void* workspace, cudaStream_t s) {
   cudaError_t e;
+  const Layout l = layout(p.n, p.d, p.bits, p.gpr, p.T, p.ntask, routed);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int sets = routed ? p.ntask : 1;
-  const int *segs = nullptr, *perm = nullptr;
+  int* segs = nullptr;
+  uint16_t* X = reinterpret_cast<uint16_t*>(ws + l.x);
   const uint16_t* a_rows = dY;
-  uint64_t rows = (uint64_t)p.T;
   if (routed) {
-    const int pos = route_positions(p.T, p.ntask);
-    int* pm = reinterpret_cast<int*>(ws);
-    int* sg = pm + pos;
-    uint16_t* g = reinterpret_cast<uint16_t*>(ws + ((size_t)(pos + 2 * p.ntask) * 4 + 255) / 256 * 256);
-    lut8_route_kernel<<<1, kRouteThreads, 0, s>>>(p.task, (int)p.T, p.ntask, pos, pm, sg, p.check);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const int64_t units = p.n / 8, total = (int64_t)pos * units;
-    lut8_gather_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(reinterpret_cast<const uint4*>(dY), pm, pos, units,
-                                                                       reinterpret_cast<uint4*>(g));
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    segs = sg;
-    perm = pm;
+    int* perm = reinterpret_cast<int*>(ws + l.perm);
+    segs = reinterpret_cast<int*>(ws + l.segs);
+    uint16_t* g = reinterpret_cast<uint16_t*>(ws + l.dy);
     a_rows = g;
-    rows = (uint64_t)pos;
-    ws += route_bytes(p.n, p.T, p.ntask);
+    lut8_route_kernel<<<1, kRouteThreads, 0, s>>>(p.task, (int)p.T, p.ntask, (int)l.rows, perm, segs, p.check);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // one grid row per position, as many as a grid has
+    auto rows_grid = [](int64_t units, int64_t rows) { return dim3((unsigned)((units + 1023) / 1024), (unsigned)rows); };
+    for (int64_t r = 0; r < l.rows; r += 65535) {
+      const int64_t rows = l.rows - r < 65535 ? l.rows - r : 65535;
+      lut8_gather_kernel<<<rows_grid(p.n / 8, rows), 256, 0, s>>>(reinterpret_cast<const uint4*>(dY), perm + r, p.n / 8,
+                                                                  reinterpret_cast<uint4*>(g + r * p.n));
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      lut8_dequant_rows_kernel<<<rows_grid(p.d / 8, rows), 256, 0, s>>>(
+          reinterpret_cast<const uint2*>(q), scale, perm + r, p.d / 8, reinterpret_cast<uint4*>(X + r * p.d));
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+  } else {
+    if ((e = launch_ckpt8_dequantize(q, scale, p.T, p.d, X, s)) != cudaSuccess) return e;
   }
-  CUtensorMap tm;
-  e = make_tmap_2d(&tm, a_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)p.n, rows, (uint64_t)p.n * 2, 64, KS,
-                   CU_TENSOR_MAP_SWIZZLE_128B);
+  CUtensorMap tm_dy, tm_x;
+  e = make_tmap_2d(&tm_dy, a_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)p.n, (uint64_t)l.rows,
+                   (uint64_t)p.n * 2, 64, KS, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  const int slots = group_slots(p.gs, p.gpr), jtiles = ceil_div(p.d, N), pairs = ceil_div(p.n, 256);
-  const int64_t stride = (int64_t)part_floats(p.n, p.d, p.bits, p.gpr);
-  float* part = reinterpret_cast<float*>(ws);
-  Lut8Args args{p.packed, p.row_bytes, q, scale, p.n, p.d, p.gs, p.T, p.gpr, slots, part, stride, p.check,
-                segs, perm, pairs};
+  e = make_tmap_2d(&tm_x, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)p.d, (uint64_t)l.rows, (uint64_t)p.d * 2, 64,
+                   KS, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  Lut8Args args{};
+  args.shape = gemm::shape_of(p.n, p.d, p.T);
+  if (!routed) gemm::split_last_round(args.shape);
+  args.packed = p.packed;
+  args.row_bytes = p.row_bytes;
+  args.n = p.n;
+  args.d = p.d;
+  args.gs = p.gs;
+  args.gpr = p.gpr;
+  args.slots = group_slots(p.gs, p.gpr);
+  args.sets = sets;
+  args.part = reinterpret_cast<float*>(ws + l.part);
+  args.part_set_stride = (int64_t)part_floats(p.n, p.d, p.bits, p.gpr);
+  args.extra = reinterpret_cast<float*>(ws + l.extra);
+  args.segs = segs;
+  args.check = p.check;
   const int64_t per_set = p.n * p.gpr * (1 << p.bits);
   // without task ids the sets beyond the first have no tokens
-  const int64_t total = per_set * sets;
   if (!routed && p.ntask > 1 && !accumulate) {
     e = cudaMemsetAsync(dlut + per_set, 0, (size_t)per_set * (p.ntask - 1) * 4, s);
     if (e != cudaSuccess) return e;
   }
+  const int64_t count = routed ? (int64_t)sets * args.shape.mt * args.shape.nt : gemm::items(args.shape);
+  const int64_t quads = per_set * sets / 4;
+  const bool cut = args.shape.split > 1;
   auto run = [&](auto kern, auto red) {
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t err = gemm::launch_pairs<8>(kern, count, s, tm_dy, tm_x, args);
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2u, (unsigned)jtiles, (unsigned)(pairs * sets));
-    cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, kern, tm, args);
-    if (err != cudaSuccess) return err;
-    const int64_t quads = total / 4;
-    red<<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(reinterpret_cast<const float4*>(part), p.n, p.gpr, p.gs, jtiles,
-                                                        slots, reinterpret_cast<float4*>(dlut), accumulate, quads,
-                                                        stride / 4);
+    red<<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(args, reinterpret_cast<float4*>(dlut), accumulate, quads);
     return cudaGetLastError();
   };
   switch (p.bits) {
-    case 2: return routed ? run(lut8_tc_kernel<2, true>, lut8_reduce_kernel<2>) : run(lut8_tc_kernel<2, false>, lut8_reduce_kernel<2>);
-    case 3: return routed ? run(lut8_tc_kernel<3, true>, lut8_reduce_kernel<3>) : run(lut8_tc_kernel<3, false>, lut8_reduce_kernel<3>);
-    default: return routed ? run(lut8_tc_kernel<4, true>, lut8_reduce_kernel<4>) : run(lut8_tc_kernel<4, false>, lut8_reduce_kernel<4>);
+    case 2: return cut ? run(lut8_tc_kernel<2>, lut8_reduce_kernel<2, true>) : run(lut8_tc_kernel<2>, lut8_reduce_kernel<2, false>);
+    case 3: return cut ? run(lut8_tc_kernel<3>, lut8_reduce_kernel<3, true>) : run(lut8_tc_kernel<3>, lut8_reduce_kernel<3, false>);
+    default: return cut ? run(lut8_tc_kernel<4>, lut8_reduce_kernel<4, true>) : run(lut8_tc_kernel<4>, lut8_reduce_kernel<4, false>);
   }
 }
 

@@ -124,12 +124,17 @@ struct Plan {
   __device__ __forceinline__ Item item(int i) const { return item_at(s, i); }
 };
 
-// Epi: struct with, for every epilogue warp and item,
+// Epi: struct with, for every epilogue warp,
+//   void start(int warp, int lane, uint8_t* scratch)
+// once, and for every item
 //   void ready(const Item&, int m0, int n0, int warp, int lane)
-// before the accumulator is waited for (loads that the tile will need), and
+// while the item before it is still to be done (loads that the tile will need),
 //   void tile(uint32_t tmem, int m0, int n0, const Item&, int warp, int lane, uint8_t* scratch)
 // when it is final: the warp's accumulator rows are m0 + 32 (warp % 4) + lane (TMEM
 // lanes), columns n0 .. n0 + tn - 1; an item without K steps has no accumulator.
+//   void take()
+// between an item's ready() and its tile(): what ready() loaded is now the tile's,
+// and the next ready() follows;
 //   void done(int lane)
 // once, before the CTA leaves.  `scratch` is the 32 KB of shared memory that the
 // epilogue has to itself.
@@ -180,8 +185,10 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
     if (lane == 0) {
       int it = 0;
       const uint32_t bytes = 2u * (A_BYTES + half_n * KS * 2);             // both CTAs' operands of a step
+      Item next = pair < count ? plan.item(pair) : Item{};
       for (int i = pair; i < count && !*abort_flag; i += pairs) {
-        const Item w = plan.item(i);
+        const Item w = next;
+        if (i + pairs < count) next = plan.item(i + pairs);   // its arithmetic under this item's waits
         const int m0 = w.m * TM + 128 * rank, n0 = w.n * tn + half_n * rank;
         for (int k = w.k0; k < w.k1; ++k, ++it) {
           const int s = it % S;
@@ -213,8 +220,10 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
     if (rank == 0 && lane == 0) {
       int it = 0, j = 0;
       bool ok = true;
+      Item next = pair < count ? plan.item(pair) : Item{};
       for (int i = pair; i < count && ok; i += pairs, ++j) {
-        const Item w = plan.item(i);
+        const Item w = next;
+        if (i + pairs < count) next = plan.item(i + pairs);
         const int b = j & 1;
         if (*abort_flag || !tc::mbar_wait(&acc_empty[b], ((j >> 1) & 1) ^ 1, check)) { *abort_flag = 1; break; }
         tc::tc_fence_after();
@@ -239,17 +248,27 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
     }
   } else {
     const uint32_t acc_empty_even = tc::mapa(&acc_empty[0], 0);
+    uint8_t* scratch = smem + SCRATCH_OFF;
+    epi.start(warp, lane, scratch);
+    Item next{};
+    if (pair < count) {
+      next = plan.item(pair);
+      epi.ready(next, next.m * TM + 128 * rank, next.n * tn, warp, lane);
+    }
     int j = 0;
     for (int i = pair; i < count; i += pairs, ++j) {
       const int b = j & 1;
-      const Item w = plan.item(i);
-      const int m0 = w.m * TM + 128 * rank, n0 = w.n * tn;
-      epi.ready(w, m0, n0, warp, lane);
+      const Item w = next;
+      epi.take();
+      if (i + pairs < count) {
+        next = plan.item(i + pairs);
+        epi.ready(next, next.m * TM + 128 * rank, next.n * tn, warp, lane);
+      }
       bool have = !*abort_flag && tc::mbar_wait(&acc_full[b], (j >> 1) & 1, check);
       have = __all_sync(0xffffffffu, have);   // tcgen05.ld is warp-collective
       if (!have) { *abort_flag = 1; break; }
       tc::tc_fence_after();
-      epi.tile(tc::tmem_addr(tmem, 32 * (warp & 3), b * TN), m0, n0, w, warp, lane, smem + SCRATCH_OFF);
+      epi.tile(tc::tmem_addr(tmem, 32 * (warp & 3), b * TN), w.m * TM + 128 * rank, w.n * tn, w, warp, lane, scratch);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_cluster(acc_empty_even + 8 * b);

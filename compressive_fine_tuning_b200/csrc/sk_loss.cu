@@ -76,7 +76,9 @@ struct LogitEpi {
   unsigned int* check;
   gemm::SlabWriter out;
 
+  __device__ __forceinline__ void start(int, int, uint8_t*) {}
   __device__ __forceinline__ void ready(const gemm::Item&, int, int, int, int) {}
+  __device__ __forceinline__ void take() {}
   __device__ __forceinline__ void done(int lane) { out.drain(lane); }
   __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, const gemm::Item&, int warp, int lane,
                                        uint8_t* scratch) {
@@ -230,7 +232,9 @@ struct GradEpi {
   unsigned int* check;
   gemm::SlabWriter out;
 
+  __device__ __forceinline__ void start(int, int, uint8_t*) {}
   __device__ __forceinline__ void ready(const gemm::Item&, int, int, int, int) {}
+  __device__ __forceinline__ void take() {}
   __device__ __forceinline__ void done(int lane) { out.drain(lane); }
   __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, const gemm::Item& item, int warp, int lane,
                                        uint8_t* scratch) {

@@ -116,8 +116,16 @@ struct BinEpi {
   static constexpr int K = 1 << BITS, HB = TN / 64;
   static constexpr int COPY = K * 1024;              // bytes between a thread's copies
   const Lut8Args& a;
-  Chunk<BITS> chunks[HB];            // the row's indices of this half tile
+  Chunk<BITS> chunks[HB], coming[HB];   // the row's indices of this half tile and of the next
 
+  // the bins start at zero and every flush leaves them there
+  __device__ __forceinline__ void start(int warp, int lane, uint8_t* scratch) {
+    clear(tc::smem_u32(scratch) + 4 * (32 * warp + lane));
+  }
+  __device__ __forceinline__ void take() {
+#pragma unroll
+    for (int b = 0; b < HB; ++b) chunks[b] = coming[b];
+  }
   __device__ __forceinline__ void ready(const gemm::Item&, int m0, int n0, int warp, int lane) {
     const int64_t row = m0 + 32 * (warp & 3) + lane;
     const int64_t c0 = n0 + 128 * (warp >> 2);
@@ -125,7 +133,7 @@ struct BinEpi {
     const uint8_t* src = a.packed + row * a.row_bytes;
 #pragma unroll
     for (int b = 0; b < HB; ++b)
-      if (c0 + 32 * b < a.d) chunks[b] = load_chunk<BITS>(src, (c0 >> 5) + b);
+      if (c0 + 32 * b < a.d) coming[b] = load_chunk<BITS>(src, (c0 >> 5) + b);
   }
   __device__ __forceinline__ void done(int) {}
 
@@ -153,8 +161,7 @@ struct BinEpi {
     const int quad = warp & 3, half = warp >> 2;
     const int64_t row = m0 + 32 * quad + lane;
     const bool have = it.k1 > it.k0;                   // a set without tokens: zeros
-    const uint32_t bins = tc::smem_u32(scratch) + 4 * (128 * half + 32 * quad + lane);
-    clear(bins);
+    const uint32_t bins = tc::smem_u32(scratch) + 4 * (32 * warp + lane);
     // where this tile's partial bins go
     float* dst;
     if (a.segs == nullptr && it.part >= 0 && it.part % a.shape.split != 0) {
@@ -225,7 +232,7 @@ template <int BITS>
 __global__ void __launch_bounds__(gemm::threads(8), 1)
 lut8_tc_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x,
                const __grid_constant__ Lut8Args a) {
-  BinEpi<BITS> epi{a, {}};
+  BinEpi<BITS> epi{a, {}, {}};
   gemm::run<1, 1, 8>(&tm_dy, &tm_x, Lut8Plan{a}, epi, a.check);
 }
 
@@ -270,87 +277,98 @@ __global__ void __launch_bounds__(256) lut8_reduce_kernel(const __grid_constant_
 
 constexpr int kRouteThreads = 1024;
 
-// One CTA: count every set's tokens, lay the segments out at multiples of KS,
-// then place the tokens tile by tile (one per thread): a token's position is
-// its set's running offset plus its rank among the set's tokens of the tile
-// (earlier warps' counts, then the lanes before it), so the order within a set
-// is the token order and sums over it never depend on timing.
+// One CTA.  A warp owns a contiguous range of tokens: it counts its tokens of
+// every set, the counts are laid out set after set (segments at multiples of KS)
+// and warp after warp within a set, and the warp places its tokens in order.  The
+// order within a set is the token order, so sums over it never depend on timing.
 __global__ void __launch_bounds__(kRouteThreads) lut8_route_kernel(const int32_t* __restrict__ task, int T, int ntask,
                                                                    int positions, int* __restrict__ perm,
                                                                    int* __restrict__ segs, unsigned int* check) {
-  __shared__ int cur[kMaxRouteTasks];
-  __shared__ uint16_t per_warp[32][kMaxRouteTasks];
+  __shared__ int at[32][kMaxRouteTasks];        // the warp's count, then its next position, of a set
+  __shared__ int total[kMaxRouteTasks];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < ntask; i += kRouteThreads) cur[i] = 0;
+  const int per = ((T + 31) / 32 + 31) / 32 * 32;
+  const int t0 = (int)min((int64_t)warp * per, (int64_t)T), t1 = (int)min((int64_t)t0 + per, (int64_t)T);
+  for (int i = lane; i < ntask; i += 32) at[warp][i] = 0;
   for (int p = tid; p < positions; p += kRouteThreads) perm[p] = -1;
+  __syncwarp();
+  bool bad = false;
+  // each token once per pass; the lanes of one set agree through their lowest
+  auto each = [&](auto f) {
+#pragma unroll 4
+    for (int b = t0; b < t1; b += 32) {
+      const int t = b + lane;
+      int tau = t < t1 ? __ldg(task + t) : -1;
+      if (tau < 0 || tau >= ntask) {
+        bad = bad || t < t1;
+        tau = -1;
+      }
+      const uint32_t same = __match_any_sync(0xffffffffu, tau);
+      f(t, tau, same);
+      __syncwarp();
+    }
+  };
+  each([&](int, int tau, uint32_t same) {
+    if (tau >= 0 && lane == __ffs(same) - 1) at[warp][tau] += __popc(same);
+  });
+  if (bad) atomicOr(check, SK_CHECK_TASK_RANGE);   // left out of every LUT set's gradient
   __syncthreads();
-  for (int t = tid; t < T; t += kRouteThreads) {
-    const int tau = task[t];
-    if (tau >= 0 && tau < ntask) atomicAdd(&cur[tau], 1);
-    else atomicOr(check, SK_CHECK_TASK_RANGE);   // left out of every LUT set's gradient
+  for (int i = tid; i < ntask; i += kRouteThreads) {
+    int c = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int mine = at[w][i];
+      at[w][i] = c;
+      c += mine;
+    }
+    total[i] = c;
   }
   __syncthreads();
   if (tid == 0) {
-    int at = 0;
+    int pos = 0;
     for (int tau = 0; tau < ntask; ++tau) {
-      const int c = cur[tau];
-      segs[2 * tau] = at;
+      const int c = total[tau];
+      segs[2 * tau] = pos;
       segs[2 * tau + 1] = c;
-      cur[tau] = at;
-      at += (c + KS - 1) / KS * KS;
+      total[tau] = pos;
+      pos += (c + KS - 1) / KS * KS;
     }
   }
-  for (int base = 0; base < T; base += kRouteThreads) {
-    for (int i = tid; i < 32 * kMaxRouteTasks; i += kRouteThreads) (&per_warp[0][0])[i] = 0;
-    __syncthreads();
-    const int t = base + tid;
-    int tau = t < T ? task[t] : -1;
-    if (tau < 0 || tau >= ntask) tau = -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, tau);
-    const int before = __popc(same & ((1u << lane) - 1u));
-    if (tau >= 0 && before == 0) per_warp[warp][tau] = (uint16_t)__popc(same);
-    __syncthreads();
+  __syncthreads();
+  each([&](int t, int tau, uint32_t same) {
+    int p = 0;
     if (tau >= 0) {
-      int p = cur[tau] + before;
-      for (int w = 0; w < warp; ++w) p += per_warp[w][tau];
+      p = total[tau] + at[warp][tau] + __popc(same & ((1u << lane) - 1u));
       perm[p] = t;
     }
-    __syncthreads();
-    for (int i = tid; i < ntask; i += kRouteThreads) {
-      int c = 0;
-      for (int w = 0; w < 32; ++w) c += per_warp[w][i];
-      cur[i] += c;
-    }
-    __syncthreads();
-  }
+    __syncwarp();
+    if (tau >= 0 && lane == __ffs(same) - 1) at[warp][tau] += __popc(same);
+  });
 }
 
-// dY rows in task order, zero rows between the segments.
-__global__ void __launch_bounds__(256) lut8_gather_kernel(const uint4* __restrict__ src, const int* __restrict__ perm,
-                                                          int64_t units, uint4* __restrict__ dst) {
+// Both operands in task order, one position per grid row, zero rows between the
+// segments: dY's rows copied, the checkpoint's rows as bf16.
+__global__ void __launch_bounds__(256) lut8_gather_kernel(const uint4* __restrict__ dY, const uint2* __restrict__ q,
+                                                          const uint8_t* __restrict__ scale, const int* __restrict__ perm,
+                                                          int64_t dy_units, int64_t x_units, uint4* __restrict__ dYp,
+                                                          uint4* __restrict__ X) {
   const int64_t p = blockIdx.y;
   const int t = perm[p];
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256)
-    dst[p * units + u] = t >= 0 ? __ldg(src + (int64_t)t * units + u) : make_uint4(0u, 0u, 0u, 0u);
-}
-
-// The checkpoint's rows as bf16 in task order, zero rows between the segments.
-__global__ void __launch_bounds__(256) lut8_dequant_rows_kernel(const uint2* __restrict__ q,
-                                                                const uint8_t* __restrict__ scale,
-                                                                const int* __restrict__ perm, int64_t units,
-                                                                uint4* __restrict__ X) {
-  const int64_t p = blockIdx.y;
-  const int t = perm[p];
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < dy_units + x_units; u += (int64_t)gridDim.x * 256) {
     uint4 o = make_uint4(0u, 0u, 0u, 0u);
-    if (t >= 0) {
-      const int64_t at = (int64_t)t * units + u;
-      const uint2 v = __ldg(q + at);
-      const uint32_t s2 = ckpt8_scale2(__ldg(scale + (at >> 2)));
-      ckpt8_dequant4(v.x, s2, o.x, o.y);
-      ckpt8_dequant4(v.y, s2, o.z, o.w);
+    if (u < dy_units) {
+      if (t >= 0) o = __ldg(dY + (int64_t)t * dy_units + u);
+      dYp[p * dy_units + u] = o;
+    } else {
+      const int64_t v = u - dy_units;
+      if (t >= 0) {
+        const int64_t at = (int64_t)t * x_units + v;
+        const uint2 b = __ldg(q + at);
+        const uint32_t s2 = ckpt8_scale2(__ldg(scale + (at >> 2)));
+        ckpt8_dequant4(b.x, s2, o.x, o.y);
+        ckpt8_dequant4(b.y, s2, o.z, o.w);
+      }
+      X[p * x_units + v] = o;
     }
-    X[p * units + u] = o;
   }
 }
 
@@ -477,14 +495,12 @@ cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* sca
     lut8_route_kernel<<<1, kRouteThreads, 0, s>>>(p.task, (int)p.T, p.ntask, (int)l.rows, perm, segs, p.check);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // one grid row per position, as many as a grid has
-    auto rows_grid = [](int64_t units, int64_t rows) { return dim3((unsigned)((units + 1023) / 1024), (unsigned)rows); };
+    const int64_t units = (p.n + p.d) / 8;
     for (int64_t r = 0; r < l.rows; r += 65535) {
       const int64_t rows = l.rows - r < 65535 ? l.rows - r : 65535;
-      lut8_gather_kernel<<<rows_grid(p.n / 8, rows), 256, 0, s>>>(reinterpret_cast<const uint4*>(dY), perm + r, p.n / 8,
-                                                                  reinterpret_cast<uint4*>(g + r * p.n));
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      lut8_dequant_rows_kernel<<<rows_grid(p.d / 8, rows), 256, 0, s>>>(
-          reinterpret_cast<const uint2*>(q), scale, perm + r, p.d / 8, reinterpret_cast<uint4*>(X + r * p.d));
+      lut8_gather_kernel<<<dim3((unsigned)((units + 1023) / 1024), (unsigned)rows), 256, 0, s>>>(
+          reinterpret_cast<const uint4*>(dY), reinterpret_cast<const uint2*>(q), scale, perm + r, p.n / 8, p.d / 8,
+          reinterpret_cast<uint4*>(g + r * p.n), reinterpret_cast<uint4*>(X + r * p.d));
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
   } else {

@@ -18,14 +18,16 @@ namespace gemm {
 
 constexpr int TM = 256, TN = 256, KS = 64;
 constexpr int A_BYTES = 128 * KS * 2, B_BYTES = 128 * KS * 2, STAGE = A_BYTES + B_BYTES;
-constexpr int S = 6;
 constexpr int SLAB = 32 * 128;                    // one warp's output slab: 32 rows x 128 bytes
-constexpr int SCRATCH_OFF = S * STAGE;            // the epilogue's own memory (two slabs for each of four warps)
-constexpr int SCRATCH = 8 * SLAB;
-constexpr int BAR_OFF = SCRATCH_OFF + SCRATCH;
-constexpr int SMEM = 1024 + BAR_OFF + 256;
 constexpr int TMEM_COLS = 512;
-static_assert(SMEM <= 232448, "one CTA's shared memory");
+
+// S stages of operands (the rest of the CTA's shared memory is the epilogue's)
+template <int S>
+struct Smem {
+  static constexpr int SCRATCH_OFF = S * STAGE, SCRATCH = (7 - S) * STAGE;
+  static constexpr int BAR_OFF = SCRATCH_OFF + SCRATCH, BYTES = 1024 + BAR_OFF + 256;
+  static_assert(BYTES <= 232448, "one CTA's shared memory");
+};
 
 // EW epilogue warps (4 or 8: warps w and w + 4 see the same accumulator rows),
 // then one warp for the copies and one for the MMAs.
@@ -136,9 +138,9 @@ struct Plan {
 // between an item's ready() and its tile(): what ready() loaded is now the tile's,
 // and the next ready() follows;
 //   void done(int lane)
-// once, before the CTA leaves.  `scratch` is the 32 KB of shared memory that the
-// epilogue has to itself.
-template <int A_MN, int B_MN, int EW, class P, class Epi>
+// once, before the CTA leaves.  `scratch` is the shared memory that the epilogue has
+// to itself (32 KB with six stages, 64 KB with five).
+template <int A_MN, int B_MN, int EW, int S, class P, class Epi>
 __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* tm_b, const P& plan, Epi& epi,
                                     unsigned int* check) {
   constexpr int TMA_WARP = EW, MMA_WARP = EW + 1;
@@ -146,7 +148,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
   const uint32_t idesc = tc::idesc_bf16(TM, tn, A_MN, B_MN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + BAR_OFF);   // even CTA: both CTAs' operands landed
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem<S>::BAR_OFF);   // even CTA: both CTAs' operands landed
   uint64_t* empty = full + S;                                      // both CTAs: the pair MMAs read the stage
   uint64_t* acc_full = empty + S;                                  // both CTAs: accumulator b final
   uint64_t* acc_empty = acc_full + 2;                              // even CTA: both CTAs drained accumulator b
@@ -248,7 +250,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
     }
   } else {
     const uint32_t acc_empty_even = tc::mapa(&acc_empty[0], 0);
-    uint8_t* scratch = smem + SCRATCH_OFF;
+    uint8_t* scratch = smem + Smem<S>::SCRATCH_OFF;
     epi.start(warp, lane, scratch);
     Item next{};
     if (pair < count) {
@@ -319,15 +321,15 @@ inline void split_last_round(Shape& s) {
 }
 
 // One CTA pair per two SMs, or fewer when there are fewer items.
-template <int EW, class Kern, class... Args>
+template <int EW, int S, class Kern, class... Args>
 cudaError_t launch_pairs(Kern kern, int64_t count, cudaStream_t s, const Args&... args) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<S>::BYTES);
   if (e != cudaSuccess) return e;
   const int64_t pairs = num_sms() / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)(count < pairs ? count : pairs), 1, 1);
   cfg.blockDim = dim3(threads(EW), 1, 1);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.dynamicSmemBytes = Smem<S>::BYTES;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -159,7 +159,7 @@ logit_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ C
              const __grid_constant__ CUtensorMap tm_e, LogitArgs a) {
   LogitEpi epi{&tm_e, a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.tn,
                a.store != 0, a.check, {}};
-  gemm::run<0, 0, 4>(&tm_h, &tm_w, gemm::Plan{a.shape}, epi, a.check);
+  gemm::run<0, 0, 4, 6>(&tm_h, &tm_w, gemm::Plan{a.shape}, epi, a.check);
 }
 
 // ----------------------------------------------------------------------------
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(gemm::threads(4), 1)
 grad_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
             const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ GradArgs a) {
   GradEpi epi{&tm_out, a.out, a.parts, a.check, {}};
-  gemm::run<A_MN, 1, 4>(&tm_a, &tm_b, gemm::Plan{a.shape}, epi, a.check);
+  gemm::run<A_MN, 1, 4, 6>(&tm_a, &tm_b, gemm::Plan{a.shape}, epi, a.check);
 }
 
 // Joins the parts of the tiles that were cut along K, in part order: block
@@ -549,9 +549,9 @@ cudaError_t launch_join(const GradArgs& a, uint16_t* out, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-#define SK_TRY(x)                       \
+#define SK_TRY(...)                     \
   do {                                  \
-    cudaError_t e_ = (x);               \
+    cudaError_t e_ = (__VA_ARGS__);     \
     if (e_ != cudaSuccess) return e_;   \
   } while (0)
 
@@ -596,7 +596,7 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, shape.tn / 2));
     LogitArgs la{shape, stats, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
                  grads ? 1 : 0, a.check};
-    SK_TRY(gemm::launch_pairs<4>(logit_kernel, gemm::items(la.shape), s, tm_h, tm_w, tm_e, la));
+    SK_TRY(gemm::launch_pairs<4, 6>(logit_kernel, gemm::items(la.shape), s, tm_h, tm_w, tm_e, la));
     lse_kernel<<<(unsigned)((T + 7) / 8), dim3(8, 32), 0, s>>>(stats, nll, target, a.target64, a.ignore_index,
                                                                  (int)T, a.V, shape.nt, lse, losses ? losses + t0 : nullptr,
                                                                  a.check);
@@ -614,7 +614,7 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
       GradArgs ga{gemm::shape_of(T, a.d, a.V),
                   {nullptr, 0, 1, T, a.d, {rest, a.W, target, a.target64, a.V, a.d, a.ignore_index}}, parts, a.check};
       gemm::split_last_round(ga.shape);
-      SK_TRY(gemm::launch_pairs<4>(grad_kernel<0>, gemm::items(ga.shape), s, tm_p, tm_w_mn, tm_dh, ga));
+      SK_TRY(gemm::launch_pairs<4, 6>(grad_kernel<0>, gemm::items(ga.shape), s, tm_p, tm_w_mn, tm_dh, ga));
       SK_TRY(launch_join(ga, a.dH + t0 * a.d, s));
     }
     if (dw) {
@@ -623,7 +623,7 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
       SK_TRY(map_rows(&tm_hm, H, T, a.d, a.d, 64, 64));
       GradArgs ga{gemm::shape_of(a.V, a.d, T), {acc, t0 > 0 ? 1 : 0, t0 + T >= a.T ? 1 : 0, a.V, a.d, {}}, parts, a.check};
       gemm::split_last_round(ga.shape);
-      SK_TRY(gemm::launch_pairs<4>(grad_kernel<1>, gemm::items(ga.shape), s, tm_p, tm_hm, tm_dw, ga));
+      SK_TRY(gemm::launch_pairs<4, 6>(grad_kernel<1>, gemm::items(ga.shape), s, tm_p, tm_hm, tm_dw, ga));
       SK_TRY(launch_join(ga, a.dW, s));
     }
   }

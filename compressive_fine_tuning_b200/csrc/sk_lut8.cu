@@ -31,8 +31,11 @@ namespace {
 using gemm::KS;
 using gemm::TN;
 
-constexpr int COPIES = 2;              // copies of the bins per epilogue thread
-static_assert(COPIES * 16 * 256 * 4 <= gemm::SCRATCH, "the bins fit the epilogue's shared memory");
+constexpr int COPIES = 4;              // copies of the bins per epilogue thread
+// operand stages: 16 bins of 256 threads in four copies take the sixth stage's place
+constexpr int stages(int bits) { return bits == 4 ? 5 : 6; }
+static_assert(COPIES * 16 * 256 * 4 <= gemm::Smem<stages(4)>::SCRATCH && COPIES * 8 * 256 * 4 <= gemm::Smem<stages(3)>::SCRATCH,
+              "the bins fit the epilogue's shared memory");
 
 // Group slots of one 256-column tile.
 __host__ __device__ inline int group_slots(int64_t gs, int gpr) {
@@ -137,19 +140,37 @@ struct BinEpi {
   }
   __device__ __forceinline__ void done(int) {}
 
-  // The sums of a group: out, and the bins to zero.  `both`: the other half's too
-  // (512 bytes further on; it zeroes its own).
-  __device__ __forceinline__ void flush(uint32_t bins, float4* out, bool write, bool both) {
+  // The sums of a group: out, and the bins to zero.
+  __device__ __forceinline__ void flush(uint32_t bins, float4* out, bool write) {
 #pragma unroll 1
-    for (int c4 = 0; c4 < K / 4; ++c4, bins += 4096, ++out) {
+    for (int c4 = 0; c4 < K / 4; ++c4, bins += 4096) {
       float v[4];
       unroll<4>([&](auto e) {
-        v[e] = lds<e * 1024>(bins) + lds<e * 1024 + COPY>(bins);
-        sts<e * 1024>(bins, 0.f);
-        sts<e * 1024 + COPY>(bins, 0.f);
+        v[e] = (lds<e * 1024>(bins) + lds<e * 1024 + COPY>(bins)) + (lds<e * 1024 + 2 * COPY>(bins) + lds<e * 1024 + 3 * COPY>(bins));
       });
-      if (both) unroll<4>([&](auto e) { v[e] += lds<e * 1024 + 512>(bins) + lds<e * 1024 + 512 + COPY>(bins); });
-      if (write) *out = make_float4(v[0], v[1], v[2], v[3]);
+      unroll<4>([&](auto e) { unroll<COPIES>([&](auto k) { sts<e * 1024 + k * COPY>(bins, 0.f); }); });
+      if (write) out[c4] = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  // The same for a group of both halves (`low`: the lower half's bins, the upper's
+  // are 512 bytes further on): each half takes every other four bins.
+  __device__ __forceinline__ void flush_both(uint32_t low, int half, float4* out, bool write) {
+    low += 4096 * half;
+#pragma unroll 1
+    for (int c4 = half; c4 < K / 4; c4 += 2, low += 8192) {
+      float v[4];
+      unroll<4>([&](auto e) {
+        v[e] = (lds<e * 1024>(low) + lds<e * 1024 + COPY>(low)) + (lds<e * 1024 + 2 * COPY>(low) + lds<e * 1024 + 3 * COPY>(low));
+        v[e] += (lds<e * 1024 + 512>(low) + lds<e * 1024 + 512 + COPY>(low)) +
+                (lds<e * 1024 + 512 + 2 * COPY>(low) + lds<e * 1024 + 512 + 3 * COPY>(low));
+      });
+      unroll<4>([&](auto e) {
+        unroll<COPIES>([&](auto k) {
+          sts<e * 1024 + k * COPY>(low, 0.f);
+          sts<e * 1024 + 512 + k * COPY>(low, 0.f);
+        });
+      });
+      if (write) out[c4] = make_float4(v[0], v[1], v[2], v[3]);
     }
   }
   __device__ __forceinline__ void clear(uint32_t bins) {
@@ -175,24 +196,21 @@ struct BinEpi {
     const int c0 = n0 + 128 * half;
     const int nb = a.d <= c0 ? 0 : a.d - c0 < 128 ? (int)(a.d - c0) / 32 : HB;     // chunks of this half
     // a group on both sides of the border: the two warps of these rows meet when
-    // each has all of its share, and again when the lower one has read the upper's
+    // each has all of its share, and again when the bins are zero
     const int border = n0 + 128;
     const bool shared_g = border < a.d && border % gs != 0;
-    auto meet = [&] { tc::named_bar_sync(1 + quad, 64); };
     int g = c0 / gs, g_end = (g + 1) * gs;
-    bool waiting = half == 1 && shared_g;              // this half's first group belongs to the lower one
+    bool first = true;
     auto finish = [&](bool last) {
-      if (waiting) {
-        meet();
-        meet();
-        clear(bins);
-        waiting = false;
+      float4* out = reinterpret_cast<float4*>(dst + (g - first_g) * K);
+      if (shared_g && (half ? first : last)) {
+        tc::named_bar_sync(1 + quad, 64);
+        flush_both(bins - 512 * half, half, out, row < a.n);
+        tc::named_bar_sync(1 + quad, 64);
       } else {
-        const bool both = last && half == 0 && shared_g;
-        if (both) meet();
-        flush(bins, reinterpret_cast<float4*>(dst + (g - first_g) * K), row < a.n, both);
-        if (both) meet();
+        flush(bins, out, row < a.n);
       }
+      first = false;
     };
     // one copy of the code for all chunks: instruction fetches count here
     // (unrolled over the chunks: 8 % slower)
@@ -218,11 +236,12 @@ struct BinEpi {
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = 0u;
       }
-      unroll<16>([&](auto e2) {
-        const uint32_t at0 = bins + index_1024<BITS>(ch, 2 * e2), at1 = bins + index_1024<BITS>(ch, 2 * e2 + 1);
-        const float s0 = lds<0>(at0), s1 = lds<COPY>(at1);
-        sts<0>(at0, s0 + __uint_as_float(v[2 * e2]));
-        sts<COPY>(at1, s1 + __uint_as_float(v[2 * e2 + 1]));
+      unroll<8>([&](auto e4) {
+        uint32_t at[COPIES];
+        float sum[COPIES];
+        unroll<COPIES>([&](auto k) { at[k] = bins + index_1024<BITS>(ch, 4 * e4 + k); });
+        unroll<COPIES>([&](auto k) { sum[k] = lds<k * COPY>(at[k]); });
+        unroll<COPIES>([&](auto k) { sts<k * COPY>(at[k], sum[k] + __uint_as_float(v[4 * e4 + k])); });
       });
     }
   }
@@ -233,7 +252,7 @@ __global__ void __launch_bounds__(gemm::threads(8), 1)
 lut8_tc_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_x,
                const __grid_constant__ Lut8Args a) {
   BinEpi<BITS> epi{a, {}, {}};
-  gemm::run<1, 1, 8>(&tm_dy, &tm_x, Lut8Plan{a}, epi, a.check);
+  gemm::run<1, 1, 8, stages(BITS)>(&tm_dy, &tm_x, Lut8Plan{a}, epi, a.check);
 }
 
 // Sum the partial bins of every (set, row, group) over the column tiles that
@@ -538,16 +557,19 @@ cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* sca
   const int64_t count = routed ? (int64_t)sets * args.shape.mt * args.shape.nt : gemm::items(args.shape);
   const int64_t quads = per_set * sets / 4;
   const bool cut = args.shape.split > 1;
-  auto run = [&](auto kern, auto red) {
-    cudaError_t err = gemm::launch_pairs<8>(kern, count, s, tm_dy, tm_x, args);
+  auto go = [&](auto bits) {
+    constexpr int B = decltype(bits)::value;
+    cudaError_t err = gemm::launch_pairs<8, stages(B)>(lut8_tc_kernel<B>, count, s, tm_dy, tm_x, args);
     if (err != cudaSuccess) return err;
-    red<<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(args, reinterpret_cast<float4*>(dlut), accumulate, quads);
+    const unsigned grid = (unsigned)((quads + 255) / 256);
+    if (cut) lut8_reduce_kernel<B, true><<<grid, 256, 0, s>>>(args, reinterpret_cast<float4*>(dlut), accumulate, quads);
+    else lut8_reduce_kernel<B, false><<<grid, 256, 0, s>>>(args, reinterpret_cast<float4*>(dlut), accumulate, quads);
     return cudaGetLastError();
   };
   switch (p.bits) {
-    case 2: return cut ? run(lut8_tc_kernel<2>, lut8_reduce_kernel<2, true>) : run(lut8_tc_kernel<2>, lut8_reduce_kernel<2, false>);
-    case 3: return cut ? run(lut8_tc_kernel<3>, lut8_reduce_kernel<3, true>) : run(lut8_tc_kernel<3>, lut8_reduce_kernel<3, false>);
-    default: return cut ? run(lut8_tc_kernel<4>, lut8_reduce_kernel<4, true>) : run(lut8_tc_kernel<4>, lut8_reduce_kernel<4, false>);
+    case 2: return go(std::integral_constant<int, 2>());
+    case 3: return go(std::integral_constant<int, 3>());
+    default: return go(std::integral_constant<int, 4>());
   }
 }
 

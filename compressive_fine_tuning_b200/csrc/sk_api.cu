@@ -142,13 +142,17 @@ bool routed_dx_possible(int64_t n, int64_t d, int64_t T, int ntask) {
   return forced == 2 || T >= kBwdTcMinT;
 }
 
-// LUT gradient from a checkpoint: the same rules as the bf16 tensor-core
-// backward, for one LUT set and for several.
+// LUT gradient from a checkpoint: the tensor cores take the bf16 gradient's
+// shapes; the token count from which the tensor cores win falls with the layer's
+// size, since their time hardly depends on a few tokens: measured 11 us against
+// 10.7 (CUDA cores) at n x d = 256 x 512 and 16 tokens, 25.3 against 25.1 at
+// 4096 x 4096 and 4, 45 against 43 at 8192 x 5120 and 1; with eight LUT sets 130
+// against 174 at 4096 x 4096 and 16, 126 against 104 at 4.
 bool use_tensor_cores_lut8(int64_t n, int64_t d, int64_t T, int ntask) {
   if (ntask > sk::kMaxRouteTasks || n < 64 || d < 64) return false;
   const int forced = env_path("SK_BWD_PATH");
   if (forced == 1) return false;
-  return forced == 2 || T >= kBwdTcMinT;
+  return forced == 2 || T >= 16 || T * n * d >= (int64_t(1) << (ntask > 1 ? 27 : 26));
 }
 
 // Shape rules shared by the layer calls.
@@ -664,7 +668,7 @@ sk_status sk_layer_norm_fwd(const void* x, int xtype, int64_t T, int64_t d, cons
   unsigned int* check = nullptr;
   st = device_state(&check);
   if (st != SK_OK) return st;
-  sk::NormFwd a{x, w, b, y, mean, rstd, q, scale, T, d, eps, rms, xtype, wtype};
+  sk::NormFwd a{x, w, b, y, mean, rstd, q, scale, T, d, eps, rms, xtype, wtype, check};
   cudaError_t e = sk::launch_norm_fwd(a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "norm kernel launch");
 }
@@ -697,7 +701,7 @@ sk_status sk_layer_norm_bwd(const void* dy, const void* x, int xtype, int64_t T,
   unsigned int* check = nullptr;
   st = device_state(&check);
   if (st != SK_OK) return st;
-  sk::NormBwd a{dy, x, w, mean, rstd, dx, dw, db, static_cast<float*>(workspace), T, d, rms, xtype, wtype};
+  sk::NormBwd a{dy, x, w, mean, rstd, dx, dw, db, static_cast<float*>(workspace), T, d, rms, xtype, wtype, check};
   cudaError_t e = sk::launch_norm_bwd(a, s);
   return e == cudaSuccess ? ok() : cuda_fail(e, "norm kernel launch");
 }

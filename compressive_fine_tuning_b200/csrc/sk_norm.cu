@@ -363,6 +363,448 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormBwd a) {
   }
 }
 
+// ----------------------------------------------------------------------------
+// many rows: two at a time
+// ----------------------------------------------------------------------------
+//
+// With thousands of rows what costs is not latency but work per value: a forward
+// CTA that loads w and b (8 bytes per column in fp32, from L1) for one bf16 row of
+// 2 + 2 bytes per column spends more on them than on the row, and shuffles and
+// barriers come once per thread and row whatever the thread holds.  So these
+// kernels give a thread more columns (32 in 16 bits) and a CTA two neighbouring
+// rows, whose sums cross the warps together (four sums in six shuffles, one
+// barrier), and use packed fp32 pairs for the arithmetic.  At [8192, 4096] bf16
+// with fp32 weights, where copying the rows takes 23 us: one row per CTA and 16
+// columns per thread 33-35 us, two rows and 32 columns 27 us; more rows or more
+// columns per thread lose it again to occupancy.
+
+using f2 = uint64_t;                               // two fp32 values
+
+__device__ __forceinline__ f2 f2_of(float lo, float hi) {
+  f2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float2 f2_get(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+  const float2 r = f2_get(v);
+  return r.x + r.y;
+}
+
+// values 2 i and 2 i + 1 of eight
+template <typename T>
+__device__ __forceinline__ f2 pair_of(const Raw<T>& r, int i) {
+  return f2_of(elem(r, 2 * i), elem(r, 2 * i + 1));
+}
+template <typename T>
+__device__ __forceinline__ void pack_pairs(const f2 (&v)[4], Raw<T>& r) {
+  float e[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = f2_get(v[i]);
+    e[2 * i] = x.x;
+    e[2 * i + 1] = x.y;
+  }
+  pack8<T>(e, r);
+}
+
+// Chunks of eight columns per thread in the kernels of two rows: 32 columns in 16
+// bits, 16 in fp32 (the same registers).
+template <typename T>
+__host__ __device__ constexpr int pair_chunks() { return sizeof(T) == 2 ? 4 : 2; }
+
+// Sums of N = 2 or 4 values over the CTA, in every thread.  Within a warp the lanes
+// share the values out as they halve: N - 1 + (5 - log2 N) shuffles.  buf: [N][32]
+// floats, written again only after a later sum's barrier.
+template <int N>
+__device__ __forceinline__ void cta_sums(float (&v)[N], float* buf) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  float a;
+  int which;
+  if constexpr (N == 4) {
+    const bool up = lane & 16;
+    const float s0 = up ? v[0] : v[2], s1 = up ? v[1] : v[3];
+    const float k0 = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, s0, 16);
+    const float k1 = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, s1, 16);
+    const bool up2 = lane & 8;
+    a = (up2 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, up2 ? k0 : k1, 8);
+    which = (lane >> 4) * 2 + ((lane >> 3) & 1);
+  } else {
+    const bool up = lane & 16;
+    a = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+    a += __shfl_xor_sync(0xffffffffu, a, 8);
+    which = lane >> 4;
+  }
+  a += __shfl_xor_sync(0xffffffffu, a, 4);
+  a += __shfl_xor_sync(0xffffffffu, a, 2);
+  a += __shfl_xor_sync(0xffffffffu, a, 1);
+  if ((lane & (N == 4 ? 7 : 15)) == 0) buf[which * 32 + (threadIdx.x >> 5)] = a;
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float sum = 0.f;
+    for (int w = 0; w < warps; w += 4) {           // entries beyond the warps are zero
+      const float4 p = *reinterpret_cast<const float4*>(buf + n * 32 + w);
+      sum += (p.x + p.y) + (p.z + p.w);
+    }
+    v[n] = sum;
+  }
+}
+
+// The sums' entries beyond the last warp, up to the next four.
+__device__ __forceinline__ void clear_sums(float* buf, int n) {
+  const int warps = blockDim.x >> 5;
+  if ((warps & 3) == 0) return;
+  for (int i = threadIdx.x; i < n * 32; i += blockDim.x)
+    if ((i & 31) >= warps) buf[i] = 0.f;              // no thread writes these entries later
+}
+
+// Forward: CTA = rows 2 blockIdx.x and the next.
+template <typename T, typename WT, int MAXT, int MINB, bool RMS, bool BIAS, bool CK>
+__global__ void __launch_bounds__(MAXT, MINB) norm_fwd_pair_kernel(NormFwd a) {
+  constexpr int NC = pair_chunks<T>(), R = 2;
+  __shared__ __align__(16) float buf[2][R * 32];
+  const int lane = threadIdx.x & 31;
+  const Cols<true> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const int64_t t = (int64_t)blockIdx.x * R;
+  const bool two = a.T - t >= R;
+  const T* x = static_cast<const T*>(a.x) + t * a.d;
+  Raw<T> cur[R][NC];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (r == 0 || two) load8<T, true>(cur[r][c], x + r * a.d, C, c);
+      else cur[r][c] = Raw<T>{};
+    }
+  clear_sums(&buf[0][0], 2 * R);
+  const float inv_d = 1.f / (float)a.d;
+  float mu[R] = {0.f, 0.f}, var[R];
+  if constexpr (!RMS) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      f2 sum = f2_of(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = f2_add(sum, pair_of(cur[r][c], i));
+      mu[r] = f2_sum(sum);
+    }
+    cta_sums<R>(mu, buf[0]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) mu[r] *= inv_d;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    f2 sum = f2_of(0.f, 0.f);
+    const f2 off = f2_of(-mu[r], -mu[r]);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (C.in(c, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 v = RMS ? pair_of(cur[r][c], i) : f2_add(pair_of(cur[r][c], i), off);
+          sum = f2_fma(v, v, sum);
+        }
+      }
+    var[r] = f2_sum(sum);
+  }
+  cta_sums<R>(var, buf[1]);
+  float rs[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    rs[r] = rsqrtf(var[r] * inv_d + a.eps);
+    if (threadIdx.x == 0 && (r == 0 || two)) {
+      if (a.mean != nullptr) a.mean[t + r] = mu[r];
+      if (a.rstd != nullptr) a.rstd[t + r] = rs[r];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    Raw<WT> w, b;
+    load8<WT, true>(w, static_cast<const WT*>(a.w), C, c);
+    if constexpr (BIAS) load8<WT, true>(b, static_cast<const WT*>(a.b), C, c);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r > 0 && !two) break;
+      const f2 off = f2_of(-mu[r], -mu[r]), scale = f2_of(rs[r], rs[r]);
+      f2 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f2 xh = f2_mul(RMS ? pair_of(cur[r][c], i) : f2_add(pair_of(cur[r][c], i), off), scale);
+        if constexpr (BIAS) v[i] = f2_fma(xh, pair_of(w, i), pair_of(b, i));
+        else v[i] = f2_mul(xh, pair_of(w, i));
+      }
+      Raw<T> o;
+      pack_pairs<T>(v, o);
+      store8<T, true>(static_cast<T*>(a.y) + (t + r) * a.d, o, C, c);
+      if constexpr (CK) {
+        uint32_t byte;
+        const uint2 q8 = ckpt8_quantize8(o.w, byte);
+        if (C.in(c, 0)) {
+          const int64_t at = (t + r) * a.d + C.col(c, 0);
+          *reinterpret_cast<uint2*>(a.q + at) = q8;
+          if ((lane & 3) == 0) a.qscale[at >> 5] = (uint8_t)byte;
+        }
+      }
+    }
+  }
+}
+
+// dx alone (a norm whose weights are not trained): CTA = rows 2 blockIdx.x and the next.
+template <typename T, typename WT, int MAXT, int MINB, bool RMS>
+__global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
+  constexpr int NC = pair_chunks<T>(), R = 2;
+  __shared__ __align__(16) float buf[2 * R * 32];
+  const Cols<true> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const int64_t t = (int64_t)blockIdx.x * R;
+  const bool two = a.T - t >= R;
+  const T* x = static_cast<const T*>(a.x) + t * a.d;
+  const T* dy = static_cast<const T*>(a.dy) + t * a.d;
+  Raw<T> cx[R][NC], cd[R][NC];
+  f2 off[R], scale[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const bool there = r == 0 || two;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (there) {
+        load8<T, true>(cx[r][c], x + r * a.d, C, c);
+        load8<T, true>(cd[r][c], dy + r * a.d, C, c);
+      } else {
+        cx[r][c] = cd[r][c] = Raw<T>{};
+      }
+    }
+    const float m = RMS || !there ? 0.f : __ldg(a.mean + t + r), rs = there ? __ldg(a.rstd + t + r) : 0.f;
+    off[r] = f2_of(-m, -m);
+    scale[r] = f2_of(rs, rs);
+  }
+  clear_sums(buf, 2 * R);
+  const float inv_d = 1.f / (float)a.d;
+  float sums[2 * R];
+  {
+    f2 su[R], sux[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) su[r] = sux[r] = f2_of(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      Raw<WT> w;
+      load8<WT, true>(w, static_cast<const WT*>(a.w), C, c);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 px = pair_of(cx[r][c], i);
+          const f2 xh = f2_mul(RMS ? px : f2_add(px, off[r]), scale[r]);
+          const f2 u = f2_mul(pair_of(cd[r][c], i), pair_of(w, i));      // zero beyond the row
+          if constexpr (!RMS) su[r] = f2_add(su[r], u);
+          sux[r] = f2_fma(u, xh, sux[r]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sums[r] = f2_sum(sux[r]);
+      sums[R + r] = f2_sum(su[r]);
+    }
+  }
+  cta_sums<2 * R>(sums, buf);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    Raw<WT> w;
+    load8<WT, true>(w, static_cast<const WT*>(a.w), C, c);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r > 0 && !two) break;
+      const float m1 = sums[R + r] * inv_d, m2 = sums[r] * inv_d;
+      const f2 n1 = f2_of(-m1, -m1), n2 = f2_of(-m2, -m2);
+      f2 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f2 px = pair_of(cx[r][c], i);
+        const f2 xh = f2_mul(RMS ? px : f2_add(px, off[r]), scale[r]);
+        f2 u = f2_mul(pair_of(cd[r][c], i), pair_of(w, i));
+        if constexpr (!RMS) u = f2_add(u, n1);
+        v[i] = f2_mul(f2_fma(xh, n2, u), scale[r]);
+      }
+      Raw<T> o;
+      pack_pairs<T>(v, o);
+      store8<T, true>(static_cast<T*>(a.dx) + (t + r) * a.d, o, C, c);
+    }
+  }
+}
+
+// Backward with dw and db.  The sums over rows want few CTAs that keep their
+// columns in registers (48 of them with w), so rows come through a ring in shared
+// memory: thread 0 asks for pairs of rows ahead by bulk copies, and the values are
+// read from there for the sums and again for dx, which leaves the registers to the
+// accumulators.  A slot is asked for again after the next pair's barrier, by which
+// every thread is done with it.  At [8192, 4096] bf16 (31 us for its traffic at
+// the copy rate): one row at a time in registers 47-52 us, pairs from the ring 41 us.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
+constexpr int kMaxStages = 4;
+
+struct Ring {
+  int stages;
+  uint32_t row_bytes;      // a slot holds two rows of x and two of dy
+};
+
+template <typename T>
+__device__ __forceinline__ void take8(Raw<T>& r, const uint8_t* row, const Cols<true>& C, int c, bool there) {
+  if (there && C.in(c, 0)) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + (size_t)C.col(c, 0) * sizeof(T));
+#pragma unroll
+    for (int q = 0; q < Raw<T>::NW / 4; ++q) {
+      const uint4 v = p[q];
+      r.w[4 * q] = v.x; r.w[4 * q + 1] = v.y; r.w[4 * q + 2] = v.z; r.w[4 * q + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < Raw<T>::NW; ++q) r.w[q] = 0u;
+  }
+}
+
+template <typename T, typename WT, int MAXT, int MINB, bool RMS>
+__global__ void __launch_bounds__(MAXT, MINB) norm_bwd_ring_kernel(NormBwd a, Ring ring) {
+  constexpr int NC = 2, R = 2;
+  extern __shared__ __align__(128) uint8_t rows[];           // [stages][R rows of x, R rows of dy]
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ __align__(16) float buf[2][2 * R * 32];
+  const Cols<true> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t t = (int64_t)blockIdx.x * R;
+  const uint32_t half_slot = R * ring.row_bytes;
+  auto ask = [&](int64_t row, int s) {
+    if (row >= a.T) return;
+    const uint32_t bytes = (a.T - row >= R ? R : 1) * ring.row_bytes;
+    uint8_t* slot = rows + (size_t)s * 2 * half_slot;
+    tc::mbar_arrive_expect_tx(&full[s], 2 * bytes);
+    bulk_load(slot, x + row * a.d, bytes, &full[s]);
+    bulk_load(slot + half_slot, dy + row * a.d, bytes, &full[s]);
+  };
+  clear_sums(&buf[0][0], 2 * 2 * R);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ring.stages; ++s) tc::mbar_init(&full[s], 1);
+    tc::fence_mbar_init();
+    for (int s = 0; s + 1 < ring.stages; ++s) ask(t + s * step, s);
+  }
+  Raw<WT> w[NC];
+  f2 dw[NC][4], db[NC][4];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    load8<WT, true>(w[c], static_cast<const WT*>(a.w), C, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[c][i] = db[c][i] = f2_of(0.f, 0.f);
+  }
+  __syncthreads();
+  const float inv_d = 1.f / (float)a.d;
+  int s = 0, before = ring.stages - 1, parity = 0;
+  uint32_t phase = 0;
+  for (; t < a.T; t += step, parity ^= 1) {
+    const bool two = a.T - t >= R;
+    f2 off[R], scale[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool there = r == 0 || two;
+      const float m = RMS || !there ? 0.f : __ldg(a.mean + t + r), rs = there ? __ldg(a.rstd + t + r) : 0.f;
+      off[r] = f2_of(-m, -m);
+      scale[r] = f2_of(rs, rs);
+    }
+    if (!tc::mbar_wait(&full[s], phase, a.check)) return;
+    const uint8_t* slot = rows + (size_t)s * 2 * half_slot;
+    float sums[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      f2 su = f2_of(0.f, 0.f), sux = f2_of(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        Raw<T> vx, vd;                // beyond the row, and in a second row that is not there, zeros
+        take8<T>(vx, slot + r * ring.row_bytes, C, c, r == 0 || two);
+        take8<T>(vd, slot + half_slot + r * ring.row_bytes, C, c, r == 0 || two);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 g = pair_of(vd, i), px = pair_of(vx, i);
+          const f2 xh = f2_mul(RMS ? px : f2_add(px, off[r]), scale[r]);
+          const f2 u = f2_mul(g, pair_of(w[c], i));
+          if constexpr (!RMS) su = f2_add(su, u);
+          sux = f2_fma(u, xh, sux);
+          dw[c][i] = f2_fma(g, xh, dw[c][i]);
+          db[c][i] = f2_add(db[c][i], g);
+        }
+      }
+      sums[r] = f2_sum(sux);
+      sums[R + r] = f2_sum(su);
+    }
+    cta_sums<2 * R>(sums, buf[parity]);
+    if (threadIdx.x == 0) ask(t + (ring.stages - 1) * step, before);
+    before = s;
+    if (++s == ring.stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+    if (a.dx == nullptr) continue;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r > 0 && !two) break;
+      const float m1 = sums[R + r] * inv_d, m2 = sums[r] * inv_d;
+      const f2 n1 = f2_of(-m1, -m1), n2 = f2_of(-m2, -m2);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        Raw<T> vx, vd;
+        take8<T>(vx, slot + r * ring.row_bytes, C, c, true);
+        take8<T>(vd, slot + half_slot + r * ring.row_bytes, C, c, true);
+        f2 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 px = pair_of(vx, i);
+          const f2 xh = f2_mul(RMS ? px : f2_add(px, off[r]), scale[r]);
+          f2 u = f2_mul(pair_of(vd, i), pair_of(w[c], i));
+          if constexpr (!RMS) u = f2_add(u, n1);
+          v[i] = f2_mul(f2_fma(xh, n2, u), scale[r]);
+        }
+        Raw<T> o;
+        pack_pairs<T>(v, o);
+        store8<T, true>(static_cast<T*>(a.dx) + (t + r) * a.d, o, C, c);
+      }
+    }
+  }
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    if (C.in(c, 0)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<f2*>(part + C.col(c, 2 * i)) = dw[c][i];
+        *reinterpret_cast<f2*>(part + a.d + C.col(c, 2 * i)) = db[c][i];
+      }
+    }
+}
+
 // dw and db partials by columns, for rows too long to keep their sums in
 // registers: block (x, y) adds a range of rows for 256 columns.
 template <typename T>
@@ -427,9 +869,52 @@ cudaError_t by_types(int xt, int wt, F f) {
   return wt == SK_F32 ? f(__half(), float()) : f(__half(), __half());
 }
 
+// Shared memory of the ring: four stages where `ctas` CTAs of an SM have room for
+// them, two at least (0: no room, the register kernels take such rows).
+int ring_stages(size_t stage_bytes, int ctas) {
+  const size_t room = (size_t)(220 << 10) / ctas;
+  const size_t n = room / stage_bytes;
+  return n < 2 ? 0 : n > kMaxStages ? kMaxStages : (int)n;
+}
+
+template <class Kern, class Args>
+cudaError_t launch_ring(Kern kern, unsigned grid, int threads, size_t stage_bytes, const Ring& ring, const Args& a,
+                        cudaStream_t s) {
+  const size_t smem = stage_bytes * ring.stages;
+  if (smem > (48 << 10)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<grid, threads, smem, s>>>(a, ring);
+  return cudaGetLastError();
+}
+
+// Two rows per CTA from eight rows per SM on: below that the rows are too few to
+// fill the SMs, and one row per CTA with fewer columns per thread is sooner done
+// (one row of 8192: 2.4 against 3.6 us).
+bool pairs_of_rows(int64_t T, int64_t d) { return d > 512 && T >= 8 * (int64_t)num_sms(); }
+
 template <typename T, typename WT, bool VEC, bool CK>
 cudaError_t fwd_shape(const NormFwd& a, cudaStream_t s) {
   const int64_t sms = num_sms();
+  if constexpr (VEC) {
+    const int th = team_threads(a.d, pair_chunks<T>());
+    if (th <= 1024 && pairs_of_rows(a.T, a.d)) {
+      auto run = [&](auto kern) {
+        kern<<<(unsigned)((a.T + 1) / 2), th, 0, s>>>(a);
+        return cudaGetLastError();
+      };
+      auto shape = [&](auto rms, auto bias) {
+        constexpr bool RMS = decltype(rms)::value, BIAS = decltype(bias)::value;
+        if (th <= 128) return run(norm_fwd_pair_kernel<T, WT, 128, 5, RMS, BIAS, CK>);
+        if (th <= 256) return run(norm_fwd_pair_kernel<T, WT, 256, 2, RMS, BIAS, CK>);
+        return run(norm_fwd_pair_kernel<T, WT, 1024, 1, RMS, BIAS, CK>);
+      };
+      const std::true_type yes;
+      const std::false_type no;
+      return a.rms ? (a.b ? shape(yes, yes) : shape(yes, no)) : (a.b ? shape(no, yes) : shape(no, no));
+    }
+  }
   auto go = [&](auto kern, int threads, int64_t rows_per_cta, int64_t ctas_per_sm) {
     int64_t grid = (a.T + rows_per_cta - 1) / rows_per_cta;
     if (grid > sms * ctas_per_sm) grid = sms * ctas_per_sm;
@@ -493,7 +978,39 @@ cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
   const int64_t sms = num_sms();
   cudaError_t e;
   auto check = [&] { return cudaGetLastError(); };
-  if (dw && a.d <= kFusedDw) {
+  bool done = false;                   // dx and, up to kFusedDw, the partials of dw and db
+  if constexpr (VEC) {
+    const int th = team_threads(a.d, 2);
+    const int ctas = th <= 512 ? 512 / th : 1;
+    const size_t row = (size_t)a.d * sizeof(T);
+    const int stages = a.d <= kFusedDw ? ring_stages(4 * row, ctas) : 0;
+    const int dx_th = team_threads(a.d, pair_chunks<T>());
+    if (dw && stages >= 2 && pairs_of_rows(a.T, a.d) && parts == sms * ctas) {
+      const Ring ring{stages, (uint32_t)row};
+      auto run = [&](auto rms) {
+        constexpr bool RMS = decltype(rms)::value;
+        return th <= 256 ? launch_ring(norm_bwd_ring_kernel<T, WT, 256, 2, RMS>, (unsigned)parts, th, 4 * row, ring, a, s)
+                         : launch_ring(norm_bwd_ring_kernel<T, WT, 512, 1, RMS>, (unsigned)parts, th, 4 * row, ring, a, s);
+      };
+      e = a.rms ? run(std::true_type()) : run(std::false_type());
+      if (e != cudaSuccess) return e;
+      done = true;
+    } else if (!dw && dx_th <= 1024 && pairs_of_rows(a.T, a.d)) {
+      auto run = [&](auto kern) {
+        kern<<<(unsigned)((a.T + 1) / 2), dx_th, 0, s>>>(a);
+        return cudaGetLastError();
+      };
+      auto shape = [&](auto rms) {
+        constexpr bool RMS = decltype(rms)::value;
+        if (dx_th <= 128) return run(norm_dx_pair_kernel<T, WT, 128, 4, RMS>);
+        if (dx_th <= 256) return run(norm_dx_pair_kernel<T, WT, 256, 2, RMS>);
+        return run(norm_dx_pair_kernel<T, WT, 1024, 1, RMS>);
+      };
+      return a.rms ? shape(std::true_type()) : shape(std::false_type());
+    }
+  }
+  if (done) {
+  } else if (dw && a.d <= kFusedDw) {
     if (a.d <= 256)
       norm_bwd_kernel<T, WT, 1, 128, VEC, true, true><<<parts, 128, kWarpTeams * 2 * 256 * 4, s>>>(a);
     else if (a.d <= 512)

@@ -21,6 +21,7 @@ struct NormFwd {
   int64_t T, d;
   float eps;
   int rms, xtype, wtype;
+  unsigned int* check;
 };
 
 struct NormBwd {
@@ -35,6 +36,7 @@ struct NormBwd {
   float* part;           // [norm_bwd_parts][2][d]
   int64_t T, d;
   int rms, xtype, wtype;
+  unsigned int* check;
 };
 
 int norm_bwd_parts(int64_t T, int64_t d);

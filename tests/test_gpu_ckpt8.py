@@ -86,6 +86,8 @@ CASES = [
     (8, 32, 4, 1, 1, 1), (64, 64, 2, 2, 63, 1), (64, 64, 2, 2, 64, 1), (256, 512, 3, 4, 33, 1),
     (264, 1376, 3, 1, 300, 1), (1000, 2048, 4, 8, 129, 1), (512, 288, 2, 3, 1000, 1),
     (128, 512, 4, 4, 200, 8), (320, 1024, 3, 2, 700, 3), (64, 96, 2, 1, 5, 3), (256, 256, 4, 1, 64, 8),
+    (256, 512, 4, 16, 15, 1), (256, 512, 4, 16, 16, 1), (1024, 4096, 3, 2, 17, 5), (520, 1056, 2, 33, 100, 2),
+    (1024, 4096, 4, 1, 3000, 1), (2568, 2080, 4, 5, 2500, 1),
 ]
 
 

@@ -122,17 +122,35 @@ def test_checkpoint_of_the_output(T, d, rms):
 def test_many_rows_take_turns():
     """More rows than teams: every row goes through the loop that a team repeats."""
     from compressive_fine_tuning_b200 import sk
-    for T, d in ((20011, 64), (9001, 520), (3001, 4104)):
-        x, w, b, dy = _case(T, d, "bf16", "bf16")
-        y, mean, rstd, _ = sk.layer_norm_fwd(x.cuda(), w.cuda(), b.cuda())
+    for T, d, dt, wt, rms in ((20011, 64, "bf16", "bf16", False), (9001, 520, "bf16", "fp32", False),
+                              (3001, 4104, "bf16", "bf16", False), (1185, 1536, "fp16", "fp32", True),
+                              (1184, 2056, "fp32", "fp32", False), (2367, 5120, "bf16", "bf16", True),
+                              (1301, 8192, "bf16", "fp32", False), (1200, 8192, "fp32", "fp32", True),
+                              (1201, 9000, "bf16", "bf16", False), (1186, 17000, "fp16", "fp16", True)):
+        x, w, b, dy = _case(T, d, dt, wt)
+        xd, wd, bd, dyd = (t.cuda() for t in (x, w, b, dy))
+        y, mean, rstd, ck = sk.layer_norm_fwd(xd, wd, bd, 1e-5, rms, ckpt=dt == "bf16" and d % 32 == 0)
         X, W, B, DY = _n(x), _n(w), _n(b), _n(dy)
-        ref, mu, r = oo.norm_forward(X, W, B, 1e-5, False)
-        assert (np.abs(_n(y) - ref) <= 2.0 ** -8 * np.abs(ref) + 1e-4 * (1 + np.abs(ref))).all()
-        _, dw, db = sk.layer_norm_bwd(dy.cuda(), x.cuda(), w.cuda(), mean, rstd)
-        _, rdw, rdb = oo.norm_backward(DY, X, W, 1e-5, False)
-        mag = (np.abs(DY) * (np.abs(X - mu[:, None]) * r[:, None] + 2)).sum(0)
-        _check(dw, rdw, 2.0 ** -8 * np.abs(rdw) + (K + T) * V * mag, "dw")
-        _check(db, rdb, 2.0 ** -8 * np.abs(rdb) + (K + T) * V * np.abs(DY).sum(0), "db")
+        ref, mu, r = oo.norm_forward(X, W, B, 1e-5, rms)
+        xh = np.abs(X - mu[:, None]) * r[:, None]
+        spread = xh + xh.mean(1, keepdims=True) + (np.abs(X).mean(1) * r)[:, None]
+        _check(y, ref, HALF[dt] * np.abs(ref) + K * V * (np.abs(W) * spread + np.abs(B)) + _smallest(dt), "y")
+        _check(rstd, r, K * V * r * (1 + (np.abs(X).mean(1) * r) ** 2), "rstd")
+        if ck is not None:
+            want = sk.ckpt8(y)
+            assert torch.equal(ck.q, want.q) and torch.equal(ck.scale, want.scale)
+        dx, dw, db = sk.layer_norm_bwd(dyd, xd, wd, mean, rstd, rms)
+        rdx, rdw, rdb = oo.norm_backward(DY, X, W, 1e-5, rms)
+        u = np.abs(DY * W)
+        m2 = (u * xh).mean(1, keepdims=True)
+        lim = HALF[dt] * np.abs(rdx) + _smallest(dt)
+        lim = lim + K * V * r[:, None] * (u + (0 if rms else 1) * u.mean(1, keepdims=True) + spread * (m2 + u))
+        _check(dx, rdx, lim, "dx")
+        _check(sk.layer_norm_bwd(dyd, xd, wd, mean, rstd, rms, bias=False, need_dw=False)[0], rdx, lim, "dx alone")
+        _check(dw, rdw, HALF[wt] * np.abs(rdw) + (K + T) * V * (np.abs(DY) * spread).sum(0) + _smallest(wt), "dw")
+        _check(db, rdb, HALF[wt] * np.abs(rdb) + (K + T) * V * np.abs(DY).sum(0) + _smallest(wt), "db")
+        again = sk.layer_norm_bwd(dyd, xd, wd, mean, rstd, rms)
+        assert all(torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
 
 
 def test_large_mean_keeps_the_spread():

@@ -761,17 +761,20 @@ sk_status sk_cross_entropy(const uint16_t* H, const uint16_t* W, const void* tar
   return e == cudaSuccess ? ok() : cuda_fail(e, "cross-entropy kernel launch");
 }
 
-sk_status sk_scale_bf16(uint16_t* x, int64_t count, const float* factor, sk_stream_t stream) {
+sk_status sk_scale_bf16(uint16_t* x, int64_t nx, uint16_t* y, int64_t ny, const float* factor, sk_stream_t stream) {
   g_last_error.clear();
-  if (count < 0 || count % 8 != 0) return fail(SK_ERR_INVALID_ARG, "count must be a multiple of 8 (got %lld)", (long long)count);
-  if (count == 0) return ok();
-  if (!x || !factor) return fail(SK_ERR_INVALID_ARG, "null pointer");
-  if (!aligned16(x)) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
-  if (overlaps(x, (size_t)count * 2, factor, 4)) return fail(SK_ERR_INVALID_ARG, "output overlaps an input");
+  if (nx < 0 || nx % 8 != 0 || ny < 0 || ny % 8 != 0)
+    return fail(SK_ERR_INVALID_ARG, "sizes must be multiples of 8 (got %lld, %lld)", (long long)nx, (long long)ny);
+  if (nx + ny == 0) return ok();
+  if ((nx && !x) || (ny && !y) || !factor) return fail(SK_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(y)) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (overlaps(x, (size_t)nx * 2, factor, 4) || overlaps(y, (size_t)ny * 2, factor, 4))
+    return fail(SK_ERR_INVALID_ARG, "output overlaps an input");
+  if (overlaps(x, (size_t)nx * 2, y, (size_t)ny * 2)) return fail(SK_ERR_INVALID_ARG, "outputs overlap");
   unsigned int* check = nullptr;
   sk_status st = device_state(&check);
   if (st != SK_OK) return st;
-  cudaError_t e = sk::launch_scale_bf16(x, count, factor, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = sk::launch_scale_bf16(x, nx, y, ny, factor, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "scale kernel launch");
 }
 

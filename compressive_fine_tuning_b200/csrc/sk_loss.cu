@@ -143,6 +143,13 @@ struct LogitEpi {
   }
 };
 
+// What a chunk's kernels share besides arrays: zeroed by the logit kernel, which
+// runs before the others.
+struct Shared {
+  unsigned long long count;   // tokens that take part
+  unsigned int blocks;        // blocks of lse_kernel that are done
+};
+
 struct LogitArgs {
   gemm::Shape shape;
   float2* stats;
@@ -151,12 +158,18 @@ struct LogitArgs {
   int target64;
   int64_t ignore_index;
   int T, V, store;
+  Shared* shared;
+  int keep_count;             // an earlier kernel has counted all chunks' tokens
   unsigned int* check;
 };
 
 __global__ void __launch_bounds__(gemm::threads(4), 1)
 logit_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_w,
              const __grid_constant__ CUtensorMap tm_e, LogitArgs a) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.shared->blocks = 0;
+    if (!a.keep_count) a.shared->count = 0;
+  }
   LogitEpi epi{&tm_e, a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.tn,
                a.store != 0, a.check, {}};
   gemm::run<0, 0, 4, 6>(&tm_h, &tm_w, gemm::Plan{a.shape}, epi, a.check);
@@ -328,9 +341,10 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ GradA
 // rows
 // ----------------------------------------------------------------------------
 
-// Number of tokens that take part (one CTA).
+// Number of tokens that take part (one CTA), for a mean over several chunks: the
+// first chunk's gradients need all chunks' number.
 __global__ void __launch_bounds__(1024) count_kernel(const void* target, int target64, int64_t T, int64_t V,
-                                                     int64_t ignore, unsigned int* check, int64_t* count) {
+                                                     int64_t ignore, unsigned int* check, Shared* shared) {
   __shared__ int sums[32];
   int c = 0;
   for (int64_t t = threadIdx.x; t < T; t += 1024) c += class_of(target, target64, t, V, ignore, check) >= 0;
@@ -339,9 +353,9 @@ __global__ void __launch_bounds__(1024) count_kernel(const void* target, int tar
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = c;
   __syncthreads();
   if (threadIdx.x == 0) {
-    int64_t total = 0;
-    for (int w = 0; w < 32; ++w) total += sums[w];
-    *count = total;
+    unsigned long long total = 0;
+    for (int w = 0; w < 32; ++w) total += (unsigned long long)sums[w];
+    shared->count = total;
   }
 }
 
@@ -354,22 +368,43 @@ __device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s
   m = top;
 }
 
+struct LseArgs {
+  const float2* stats;
+  float* nll;               // the target's logits in, the losses out
+  const void* target;
+  int target64;
+  int64_t ignore_index;
+  int T, tiles;
+  int64_t V;
+  float* lse;
+  float* losses;            // [T] of this chunk, or nullptr
+  Shared* shared;
+  int count;                // add this chunk's tokens to the count
+  // the reduced loss, written by the last block of the last chunk (else nullptr):
+  // the sum of all_losses[0 .. all), divided by the count for a mean
+  float* reduced;
+  const float* all_losses;
+  int64_t all;
+  int mean;
+  unsigned int* check;
+};
+
 // lse and loss of eight tokens per block: 32 thread rows walk the vocabulary's
 // tiles, then their pairs are joined by halves.
 // The loss is (maximum - l_target) + log(sum): next to lse - l_target it keeps the
 // digits of a surely predicted token, whose maximum is the target's own logit.
-// nll: the target's logits in, the losses out.
-__global__ void __launch_bounds__(256) lse_kernel(const float2* __restrict__ stats, float* __restrict__ nll,
-                                                  const void* target, int target64, int64_t ignore, int T, int64_t V,
-                                                  int tiles, float* __restrict__ lse, float* __restrict__ losses,
-                                                  unsigned int* check) {
+// The block that finishes last sums the losses, in an order of its own, so the
+// sum does not depend on which block that is.
+__global__ void __launch_bounds__(256) lse_kernel(LseArgs a) {
   __shared__ float2 joined[32][8];
-  const int t = blockIdx.x * 8 + threadIdx.x, y = threadIdx.y;
+  __shared__ double sums[8];
+  __shared__ bool last;
+  const int t = blockIdx.x * 8 + threadIdx.x, y = threadIdx.y, tid = y * 8 + threadIdx.x;
   float m = -INFINITY, s = 0.f;
-  if (t < T) {
+  if (t < a.T) {
 #pragma unroll 4
-    for (int i = y; i < tiles; i += 32) {
-      const float2 p = stats[(int64_t)i * T + t];
+    for (int i = y; i < a.tiles; i += 32) {
+      const float2 p = a.stats[(int64_t)i * a.T + t];
       join_stats(m, s, p.x, p.y);
     }
   }
@@ -383,30 +418,43 @@ __global__ void __launch_bounds__(256) lse_kernel(const float2* __restrict__ sta
       joined[y][threadIdx.x] = make_float2(m, s);
     }
   }
-  if (y == 0 && t < T) {
-    const float ls = logf(s);
-    lse[t] = m + ls;
-    const float loss = class_of(target, target64, t, V, ignore, check) >= 0 ? (m - nll[t]) + ls : 0.f;
-    nll[t] = loss;
-    if (losses != nullptr) losses[t] = loss;
+  if (y == 0) {
+    bool keep = false;
+    if (t < a.T) {
+      const float ls = logf(s);
+      a.lse[t] = m + ls;
+      keep = class_of(a.target, a.target64, t, a.V, a.ignore_index, a.check) >= 0;
+      const float loss = keep ? (m - a.nll[t]) + ls : 0.f;
+      a.nll[t] = loss;
+      if (a.losses != nullptr) a.losses[t] = loss;
+    }
+    if (a.count) {
+      const int n = __popc(__ballot_sync(0xffu, keep));
+      if (threadIdx.x == 0 && n) atomicAdd(&a.shared->count, (unsigned long long)n);
+    }
   }
-}
-
-// Sum of the tokens' losses (one CTA, fixed order), divided by the count for the mean.
-__global__ void __launch_bounds__(1024) loss_sum_kernel(const float* __restrict__ losses, int64_t T,
-                                                        const int64_t* count, float* out) {
-  __shared__ double sums[32];
-  double s = 0.0;
-  for (int64_t t = threadIdx.x; t < T; t += 1024) s += (double)losses[t];
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+  if (a.reduced == nullptr) return;
+  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (tid == 0) last = atomicAdd(&a.shared->blocks, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double sum = 0.0;
+#pragma unroll 4
+  for (int64_t k = tid; k < a.all; k += 256) sum += (double)__ldcg(a.all_losses + k);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if ((tid & 31) == 0) sums[tid >> 5] = sum;
+  __syncthreads();
+  if (tid == 0) {
     double total = 0.0;
-    for (int w = 0; w < 32; ++w) total += sums[w];
-    if (count != nullptr) total /= (double)(*count > 0 ? *count : 1);
-    *out = (float)total;
+    for (int w = 0; w < 8; ++w) total += sums[w];
+    if (a.mean) {
+      const unsigned long long n = *reinterpret_cast<volatile unsigned long long*>(&a.shared->count);
+      total /= (double)(n > 0 ? n : 1);
+    }
+    *a.reduced = (float)total;
   }
 }
 
@@ -424,7 +472,7 @@ struct ProbArgs {
   int T, V;
   const float* dloss;
   int dloss_each;           // dloss has one value per token
-  const int64_t* count;     // divide by it (mean), or nullptr
+  const Shared* shared;     // divide by its count (mean), or nullptr
   float* rest;              // [T]: P's target entry minus its bf16
   unsigned int* check;
 };
@@ -442,7 +490,7 @@ __global__ void __launch_bounds__(kProbThreads) prob_kernel(ProbArgs a) {
   }
   float c = 1.f;
   if (a.dloss != nullptr) c = a.dloss[a.dloss_each ? t : 0];
-  if (a.count != nullptr) c /= (float)(*a.count > 0 ? *a.count : 1);
+  if (a.shared != nullptr) c /= (float)(a.shared->count > 0 ? a.shared->count : 1);
   const float z = a.lse[t];
   const float at_target = c * expm1f(-a.nll[t]);
   if (threadIdx.x == 0) a.rest[t] = at_target - __bfloat162float(__float2bfloat16_rn(at_target));
@@ -463,17 +511,19 @@ __global__ void __launch_bounds__(kProbThreads) prob_kernel(ProbArgs a) {
   }
 }
 
-// x *= factor in place, unless the factor is one
-__global__ void __launch_bounds__(256) scale_kernel(uint4* __restrict__ x, int64_t units, const float* factor) {
+// x and y (each may be empty) *= factor in place, unless the factor is one
+__global__ void __launch_bounds__(256) scale_kernel(uint4* __restrict__ x, int64_t x_units, uint4* __restrict__ y,
+                                                    int64_t y_units, const float* factor) {
   const float f = *factor;
   if (f == 1.f) return;
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-    const uint4 v = x[u];
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < x_units + y_units; u += (int64_t)gridDim.x * 256) {
+    uint4* at = u < x_units ? x + u : y + (u - x_units);
+    const uint4 v = *at;
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       w[q] = f32x2_to_bf16x2(__uint_as_float(w[q] << 16) * f, __uint_as_float(w[q] & 0xffff0000u) * f);
-    x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -492,7 +542,7 @@ int64_t chunk_tokens(int64_t T, int64_t V, bool grads) {
 
 struct Layout {
   int64_t chunk, pitch;
-  size_t e, acc, parts, stats, lse, nll, rest, losses, count, total;
+  size_t e, acc, parts, stats, lse, nll, rest, losses, shared, total;
 };
 
 Layout layout(int64_t T, int64_t V, int64_t d, bool dh, bool dw) {
@@ -514,7 +564,7 @@ Layout layout(int64_t T, int64_t V, int64_t d, bool dh, bool dw) {
   l.nll = take((size_t)l.chunk * 4);
   l.rest = take((size_t)l.chunk * 4);
   l.losses = take((size_t)T * 4);
-  l.count = take(8);
+  l.shared = take(sizeof(Shared));
   l.total = at;
   return l;
 }
@@ -573,10 +623,11 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
   float* rest = reinterpret_cast<float*>(ws + l.rest);
   float4* parts = reinterpret_cast<float4*>(ws + l.parts);
   float* losses = a.reduction == SK_CE_NONE ? a.loss : reinterpret_cast<float*>(ws + l.losses);
-  int64_t* count = reinterpret_cast<int64_t*>(ws + l.count);
+  Shared* shared = reinterpret_cast<Shared*>(ws + l.shared);
   const bool mean = a.reduction == SK_CE_MEAN;
-  if (mean) {
-    count_kernel<<<1, 1024, 0, s>>>(a.target, a.target64, a.T, a.V, a.ignore_index, a.check, count);
+  const bool count_first = mean && l.chunk < a.T;
+  if (count_first) {
+    count_kernel<<<1, 1024, 0, s>>>(a.target, a.target64, a.T, a.V, a.ignore_index, a.check, shared);
     SK_TRY(cudaGetLastError());
   }
   CUtensorMap tm_w_mn, tm_dw;
@@ -595,16 +646,17 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     CUtensorMap tm_w;
     SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, shape.tn / 2));
     LogitArgs la{shape, stats, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
-                 grads ? 1 : 0, a.check};
+                 grads ? 1 : 0, shared, count_first ? 1 : 0, a.check};
     SK_TRY(gemm::launch_pairs<4, 6>(logit_kernel, gemm::items(la.shape), s, tm_h, tm_w, tm_e, la));
-    lse_kernel<<<(unsigned)((T + 7) / 8), dim3(8, 32), 0, s>>>(stats, nll, target, a.target64, a.ignore_index,
-                                                                 (int)T, a.V, shape.nt, lse, losses ? losses + t0 : nullptr,
-                                                                 a.check);
+    const bool reduce = a.reduction != SK_CE_NONE && a.loss != nullptr && t0 + T >= a.T;
+    LseArgs le{stats, nll, target, a.target64, a.ignore_index, (int)T, shape.nt, a.V, lse, losses ? losses + t0 : nullptr,
+               shared, mean && !count_first ? 1 : 0, reduce ? a.loss : nullptr, losses, a.T, mean ? 1 : 0, a.check};
+    lse_kernel<<<(unsigned)((T + 7) / 8), dim3(8, 32), 0, s>>>(le);
     SK_TRY(cudaGetLastError());
     if (!grads) continue;
     const bool each = a.reduction == SK_CE_NONE;
     ProbArgs pa{E, l.pitch, stats, lse, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
-                each && a.dloss ? a.dloss + t0 : a.dloss, each ? 1 : 0, mean ? count : nullptr, rest, a.check};
+                each && a.dloss ? a.dloss + t0 : a.dloss, each ? 1 : 0, mean ? shared : nullptr, rest, a.check};
     prob_kernel<<<(unsigned)T, kProbThreads, 0, s>>>(pa);
     SK_TRY(cudaGetLastError());
     if (dh) {
@@ -627,17 +679,14 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
       SK_TRY(launch_join(ga, a.dW, s));
     }
   }
-  if (a.reduction != SK_CE_NONE && a.loss != nullptr) {
-    loss_sum_kernel<<<1, 1024, 0, s>>>(losses, a.T, mean ? count : nullptr, a.loss);
-    SK_TRY(cudaGetLastError());
-  }
   return cudaSuccess;
 }
 
-cudaError_t launch_scale_bf16(uint16_t* x, int64_t count, const float* factor, cudaStream_t s) {
-  const int64_t units = count / 8;
+cudaError_t launch_scale_bf16(uint16_t* x, int64_t nx, uint16_t* y, int64_t ny, const float* factor, cudaStream_t s) {
+  const int64_t units = (nx + ny) / 8;
   const int64_t blocks = (units + 255) / 256, cap = (int64_t)num_sms() * 8;
-  scale_kernel<<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, s>>>(reinterpret_cast<uint4*>(x), units, factor);
+  scale_kernel<<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, s>>>(reinterpret_cast<uint4*>(x), nx / 8,
+                                                                       reinterpret_cast<uint4*>(y), ny / 8, factor);
   return cudaGetLastError();
 }
 

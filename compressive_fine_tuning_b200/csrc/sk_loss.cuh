@@ -22,6 +22,6 @@ struct CrossEntropy {
 
 size_t cross_entropy_workspace(int64_t T, int64_t V, int64_t d, bool dh, bool dw);
 cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s);
-cudaError_t launch_scale_bf16(uint16_t* x, int64_t count, const float* factor, cudaStream_t s);
+cudaError_t launch_scale_bf16(uint16_t* x, int64_t nx, uint16_t* y, int64_t ny, const float* factor, cudaStream_t s);
 
 }  // namespace sk

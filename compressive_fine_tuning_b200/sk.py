@@ -94,7 +94,7 @@ def _load() -> ctypes.CDLL:
         "sk_layer_norm_bwd": ([vp, vp, i32, i64, i64, vp, i32, vp, vp, i32, vp, vp, vp, vp, sz, vp], i32),
         "sk_cross_entropy_workspace_bytes": ([i64, i64, i64, i32, i32], sz),
         "sk_cross_entropy": ([vp, vp, vp, i32, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp, sz, vp], i32),
-        "sk_scale_bf16": ([vp, i64, vp, vp], i32),
+        "sk_scale_bf16": ([vp, i64, vp, i64, vp, vp], i32),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -113,11 +113,17 @@ def _check(status: int) -> None:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without building a Stream object (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str, ndim: Optional[int] = None) -> None:
@@ -415,10 +421,13 @@ class Ckpt8(NamedTuple):
     scale: torch.Tensor
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device: torch.device):
     """The library works on the current device: make it the tensors' own."""
     if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(device)
 
 
@@ -599,15 +608,16 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     autograd function of x, weight and bias.  With `ckpt` it returns (y, Ckpt8 of
     y's rows) for a SketchedLinear that keeps its input in 8 bits."""
     lead = x.shape[:-1]
-    rows = x.reshape(-1, x.shape[-1]).contiguous()
+    rows = x if len(lead) == 1 and x.is_contiguous() else x.reshape(-1, x.shape[-1]).contiguous()
     if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))):
         y, _, _, ck = layer_norm_fwd(rows, weight, bias, eps, rms, ckpt, stats=False)
+    else:
+        y = LayerNormFunction.apply(rows, weight, bias, eps, rms, ckpt)
+        if ckpt:
+            y, ck = y[0], Ckpt8(y[1], y[2])
+    if len(lead) != 1:
         y = y.reshape(*lead, x.shape[-1])
-        return (y, ck) if ckpt else y
-    out = LayerNormFunction.apply(rows, weight, bias, eps, rms, ckpt)
-    if not ckpt:
-        return out.reshape(*lead, x.shape[-1])
-    return out[0].reshape(*lead, x.shape[-1]), Ckpt8(out[1], out[2])
+    return (y, ck) if ckpt else y
 
 
 class LayerNorm(torch.nn.Module):
@@ -704,9 +714,8 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         dH, dW = ctx.ready
         ctx.ready = None
         with _on(H.device):
-            for t in (dH, dW):
-                if t is not None:
-                    _check(lib.sk_scale_bf16(_ptr(t), t.numel(), _ptr(g), _stream(H.device)))
+            _check(lib.sk_scale_bf16(_ptr(dH), 0 if dH is None else dH.numel(), _ptr(dW),
+                                     0 if dW is None else dW.numel(), _ptr(g), _stream(H.device)))
         return dH, dW, None, None, None
 
 
@@ -719,12 +728,15 @@ def linear_cross_entropy(H: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
     lead = H.shape[:-1]
     if target.shape != lead:
         raise ValueError("target must hold one class per token")
-    args = (H.reshape(-1, H.shape[-1]).contiguous(), W.contiguous(), target.reshape(-1).contiguous())
+    if len(lead) == 1:
+        args = (H.contiguous(), W.contiguous(), target.contiguous())
+    else:
+        args = (H.reshape(-1, H.shape[-1]).contiguous(), W.contiguous(), target.reshape(-1).contiguous())
     if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
         loss = LinearCrossEntropyFunction.apply(*args, ignore_index, reduction)
     else:
         loss = cross_entropy(*args, ignore_index, reduction)[0]
-    return loss.reshape(lead) if reduction == "none" else loss
+    return loss.reshape(lead) if reduction == "none" and len(lead) != 1 else loss
 
 
 # ---------------------------------------------------------------------------

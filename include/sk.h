@@ -340,14 +340,15 @@ sk_status sk_layer_norm_bwd(const void* dy, const void* x, int xtype, int64_t T,
  * dW != NULL) bytes; with gradients it holds one chunk of tokens' exponentials
  * (512 MiB at most, or 256 tokens' if that is more).  Deterministic.
  *
- * sk_scale_bf16: x (bf16 [count], count % 8 == 0) times the device scalar *factor,
- * in place; a factor of exactly 1 leaves x alone.
+ * sk_scale_bf16: x (bf16 [nx]) and y (bf16 [ny]; sizes multiples of 8, either may be
+ * 0) times the device scalar *factor, in place, in one launch; a factor of exactly
+ * 1 leaves them alone.  For the gradients of a loss that something scales afterwards.
  */
 size_t sk_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t d, int want_dh, int want_dw);
 sk_status sk_cross_entropy(const uint16_t* H, const uint16_t* W, const void* target, int target_bits, int64_t T,
                            int64_t V, int64_t d, int64_t ignore_index, int reduction, const float* dloss, float* loss,
                            uint16_t* dH, uint16_t* dW, void* workspace, size_t workspace_bytes, sk_stream_t stream);
-sk_status sk_scale_bf16(uint16_t* x, int64_t count, const float* factor, sk_stream_t stream);
+sk_status sk_scale_bf16(uint16_t* x, int64_t nx, uint16_t* y, int64_t ny, const float* factor, sk_stream_t stream);
 
 /*
  * sk_bin_counts: the static bin sizes of the one-hot sketch (Eq. 1),

@@ -21,11 +21,13 @@ constexpr int A_BYTES = 128 * KS * 2, B_BYTES = 128 * KS * 2, STAGE = A_BYTES + 
 constexpr int SLAB = 32 * 128;                    // one warp's output slab: 32 rows x 128 bytes
 constexpr int TMEM_COLS = 512;
 
-// S stages of operands (the rest of the CTA's shared memory is the epilogue's)
+// S full stages of operands; the rest of the CTA's shared memory is the epilogue's.
+// Narrower tiles have smaller stages, and more of them in the same memory.
+constexpr int MAX_STAGES = 14;
 template <int S>
 struct Smem {
   static constexpr int SCRATCH_OFF = S * STAGE, SCRATCH = (7 - S) * STAGE;
-  static constexpr int BAR_OFF = SCRATCH_OFF + SCRATCH, BYTES = 1024 + BAR_OFF + 256;
+  static constexpr int BAR_OFF = SCRATCH_OFF + SCRATCH, BYTES = 1024 + BAR_OFF + 512;
   static_assert(BYTES <= 232448, "one CTA's shared memory");
 };
 
@@ -40,7 +42,9 @@ struct Item {
 
 struct Shape {
   int mt, nt, ksteps;    // tiles and K steps
+  int M;                 // rows of A: a CTA whose rows all lie beyond them loads none
   int tn;                // columns per tile: 256, or less for a K-major B (a multiple of 32)
+  int a_rows;            // rows of A that a CTA loads: 128, or less (a multiple of 8) when M is less
   int group;             // M tiles walked together (see tile_at)
   // The last wave: the `split_from`-th and later tiles are cut along K into `split`
   // parts, one per pair, so that a few left-over tiles do not keep one pair each
@@ -118,11 +122,11 @@ struct SlabWriter {
   }
 };
 
-// The items of one product.  Another plan has the same three members.
+// The items of one product.  Another plan has the same members.
 struct Plan {
   const Shape& s;
+  __device__ __forceinline__ const Shape& shape() const { return s; }
   __device__ __forceinline__ int count() const { return items(s); }
-  __device__ __forceinline__ int tn() const { return s.tn; }
   __device__ __forceinline__ Item item(int i) const { return item_at(s, i); }
 };
 
@@ -144,13 +148,16 @@ template <int A_MN, int B_MN, int EW, int S, class P, class Epi>
 __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* tm_b, const P& plan, Epi& epi,
                                     unsigned int* check) {
   constexpr int TMA_WARP = EW, MMA_WARP = EW + 1;
-  const int tn = B_MN ? TN : plan.tn(), half_n = tn / 2;
+  const int tn = B_MN ? TN : plan.shape().tn, half_n = tn / 2;
+  const int a_bytes = A_MN ? A_BYTES : plan.shape().a_rows * KS * 2, b_bytes = half_n * KS * 2;
+  const int stage = a_bytes + b_bytes;
+  const int stages = min(MAX_STAGES, S * STAGE / stage);
   const uint32_t idesc = tc::idesc_bf16(TM, tn, A_MN, B_MN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem<S>::BAR_OFF);   // even CTA: both CTAs' operands landed
-  uint64_t* empty = full + S;                                      // both CTAs: the pair MMAs read the stage
-  uint64_t* acc_full = empty + S;                                  // both CTAs: accumulator b final
+  uint64_t* empty = full + MAX_STAGES;                             // both CTAs: the pair MMAs read the stage
+  uint64_t* acc_full = empty + MAX_STAGES;                                  // both CTAs: accumulator b final
   uint64_t* acc_empty = acc_full + 2;                              // even CTA: both CTAs drained accumulator b
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -161,7 +168,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
   const int count = plan.count();
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < stages; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
     }
@@ -185,25 +192,29 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
 
   if (warp == TMA_WARP) {
     if (lane == 0) {
-      int it = 0;
-      const uint32_t bytes = 2u * (A_BYTES + half_n * KS * 2);             // both CTAs' operands of a step
+      int s = 0, filled = 0;            // the slot, and how many have been filled so far (at most `stages`)
+      uint32_t phase = 1;               // of the wait for an empty slot: the first round's pass at once
       Item next = pair < count ? plan.item(pair) : Item{};
       for (int i = pair; i < count && !*abort_flag; i += pairs) {
         const Item w = next;
         if (i + pairs < count) next = plan.item(i + pairs);   // its arithmetic under this item's waits
         const int m0 = w.m * TM + 128 * rank, n0 = w.n * tn + half_n * rank;
-        for (int k = w.k0; k < w.k1; ++k, ++it) {
-          const int s = it % S;
-          if (*abort_flag || !tc::mbar_wait(&empty[s], ((it / S) & 1) ^ 1, check)) { *abort_flag = 1; break; }
-          uint8_t* a = smem + s * STAGE;
-          uint8_t* b = a + A_BYTES;
+        // rows beyond A are not loaded: what they multiply is never looked at
+        const bool odd_a = w.m * TM + 128 < plan.shape().M, load_a = rank == 0 || odd_a;
+        const uint32_t bytes = (odd_a ? 2 : 1) * a_bytes + 2 * b_bytes;        // both CTAs' operands of a step
+        for (int k = w.k0; k < w.k1; ++k) {
+          if (*abort_flag || !tc::mbar_wait(&empty[s], phase, check)) { *abort_flag = 1; break; }
+          uint8_t* a = smem + s * stage;
+          uint8_t* b = a + a_bytes;
           if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], bytes);
           const uint32_t bar = tc::mapa(&full[s], 0);
-          if (A_MN) {
-            tc::tma_load_2d_pair(a, tm_a, bar, m0, k * KS);
-            tc::tma_load_2d_pair(a + 8192, tm_a, bar, m0 + 64, k * KS);
-          } else {
-            tc::tma_load_2d_pair(a, tm_a, bar, k * KS, m0);
+          if (load_a) {
+            if (A_MN) {
+              tc::tma_load_2d_pair(a, tm_a, bar, m0, k * KS);
+              tc::tma_load_2d_pair(a + 8192, tm_a, bar, m0 + 64, k * KS);
+            } else {
+              tc::tma_load_2d_pair(a, tm_a, bar, k * KS, m0);
+            }
           }
           if (B_MN) {
             tc::tma_load_2d_pair(b, tm_b, bar, n0, k * KS);
@@ -211,16 +222,32 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
           } else {
             tc::tma_load_2d_pair(b, tm_b, bar, k * KS, n0);
           }
+          if (filled < stages) ++filled;
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
       }
       // never leave with a copy still landing in shared memory: the pair MMAs
       // read every landed stage before they free it
       bool ok = true;
-      for (int k = it > S ? it - S : 0; k < it && ok; ++k) ok = tc::mbar_wait(&empty[k % S], (k / S) & 1, check);
+      for (int k = 0; k < filled && ok; ++k) {
+        if (filled == stages) {         // oldest first: the slots from s on
+          ok = tc::mbar_wait(&empty[s], phase, check);
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        } else {
+          ok = tc::mbar_wait(&empty[k], 0, check);
+        }
+      }
     }
   } else if (warp == MMA_WARP) {
     if (rank == 0 && lane == 0) {
-      int it = 0, j = 0;
+      int s = 0, j = 0;
+      uint32_t phase = 0;
       bool ok = true;
       Item next = pair < count ? plan.item(pair) : Item{};
       for (int i = pair; i < count && ok; i += pairs, ++j) {
@@ -230,11 +257,10 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
         if (*abort_flag || !tc::mbar_wait(&acc_empty[b], ((j >> 1) & 1) ^ 1, check)) { *abort_flag = 1; break; }
         tc::tc_fence_after();
         const uint32_t acc = tc::tmem_addr(tmem, 0, b * TN);
-        for (int k = w.k0; k < w.k1; ++k, ++it) {
-          const int s = it % S;
-          if (*abort_flag || !tc::mbar_wait(&full[s], (it / S) & 1, check)) { *abort_flag = 1; ok = false; break; }
+        for (int k = w.k0; k < w.k1; ++k) {
+          if (*abort_flag || !tc::mbar_wait(&full[s], phase, check)) { *abort_flag = 1; ok = false; break; }
           tc::tc_fence_after();
-          const uint32_t ab = tc::smem_u32(smem + s * STAGE), bb = ab + A_BYTES;
+          const uint32_t ab = tc::smem_u32(smem + s * stage), bb = ab + a_bytes;
 #pragma unroll
           for (int kk = 0; kk < KS / 16; ++kk) {
             const uint64_t ad = A_MN ? tc::sdesc(ab + kk * 2048, 8192, 1024, tc::kSwizzle128)
@@ -244,6 +270,10 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
             tc::mma_ss_pair(acc, ad, bd, idesc, (k > w.k0 || kk > 0) ? 1u : 0u);
           }
           tc::mma_commit_pair(&empty[s]);
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
         if (ok) tc::mma_commit_pair(&acc_full[b]);
       }
@@ -300,8 +330,12 @@ inline Shape shape_of(int64_t M, int64_t N, int64_t K) {
   s.mt = (int)tiles_of(M);
   s.nt = (int)tiles_of(N);
   s.ksteps = (int)((K + KS - 1) / KS);
+  s.M = (int)M;
   s.tn = TN;
-  s.group = s.mt < 16 ? s.mt : 16;
+  s.a_rows = 128;
+  // about as many M as N tiles among the pairs in flight: the fewest operand bytes
+  // per step (4 to 32 measured alike within the noise of the power cap)
+  s.group = s.mt < 8 ? s.mt : 8;
   s.split_from = s.mt * s.nt;
   s.split = 1;
   return s;

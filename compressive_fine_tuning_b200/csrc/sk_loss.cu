@@ -637,12 +637,16 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     const int64_t T = a.T - t0 < l.chunk ? a.T - t0 : l.chunk;
     const uint16_t* H = a.H + t0 * a.d;
     const void* target = static_cast<const uint8_t*>(a.target) + t0 * (a.target64 ? 8 : 4);
-    CUtensorMap tm_h, tm_e;
-    SK_TRY(map_rows(&tm_h, H, T, a.d, a.d, 64, 128));
-    tm_e = tm_h;                                   // not used without gradients
-    if (grads) SK_TRY(map_rows(&tm_e, E, T, a.V, l.pitch, 64, 32));
     gemm::Shape shape = gemm::shape_of(T, a.V, a.d);
-    if (!grads) balance_tiles(shape, a.V);
+    if (!grads) {
+      balance_tiles(shape, a.V);
+      // few tokens: load their rows only, which leaves room for more stages of W
+      if (T < 128) shape.a_rows = (int)up(T, 8);
+    }
+    CUtensorMap tm_h, tm_e;
+    SK_TRY(map_rows(&tm_h, H, T, a.d, a.d, 64, shape.a_rows));
+    if (grads) SK_TRY(map_rows(&tm_e, E, T, a.V, l.pitch, 64, 32));
+    else tm_e = tm_h;                              // not used
     CUtensorMap tm_w;
     SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, shape.tn / 2));
     LogitArgs la{shape, stats, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,

@@ -65,7 +65,7 @@ struct Lut8Plan {
   __device__ __forceinline__ int count() const {
     return a.segs == nullptr ? gemm::items(a.shape) : a.sets * a.shape.mt * a.shape.nt;
   }
-  __device__ __forceinline__ int tn() const { return TN; }
+  __device__ __forceinline__ const gemm::Shape& shape() const { return a.shape; }
   __device__ __forceinline__ int set_of(int i) const { return a.segs == nullptr ? 0 : i / (a.shape.mt * a.shape.nt); }
   __device__ __forceinline__ gemm::Item item(int i) const {
     if (a.segs == nullptr) return gemm::item_at(a.shape, i);

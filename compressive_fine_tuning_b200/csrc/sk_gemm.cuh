@@ -22,7 +22,9 @@ constexpr int SLAB = 32 * 128;                    // one warp's output slab: 32 
 constexpr int TMEM_COLS = 512;
 
 // S full stages of operands; the rest of the CTA's shared memory is the epilogue's.
-// Narrower tiles have smaller stages, and more of them in the same memory.
+// Narrower tiles have smaller stages, and more of them in the same memory.  (An MMA
+// reads 128 rows of A whatever a_rows is: what follows the rows in shared memory,
+// the last stage's scratch among it, lands in accumulator rows nobody looks at.)
 constexpr int MAX_STAGES = 14;
 template <int S>
 struct Smem {
@@ -43,8 +45,8 @@ struct Item {
 struct Shape {
   int mt, nt, ksteps;    // tiles and K steps
   int M;                 // rows of A: a CTA whose rows all lie beyond them loads none
+  int a_rows;            // rows of A per CTA and tile: 128, or fewer (a multiple of 8) for a K-major A
   int tn;                // columns per tile: 256, or less for a K-major B (a multiple of 32)
-  int a_rows;            // rows of A that a CTA loads: 128, or less (a multiple of 8) when M is less
   int group;             // M tiles walked together (see tile_at)
   // The last wave: the `split_from`-th and later tiles are cut along K into `split`
   // parts, one per pair, so that a few left-over tiles do not keep one pair each
@@ -149,8 +151,8 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
                                     unsigned int* check) {
   constexpr int TMA_WARP = EW, MMA_WARP = EW + 1;
   const int tn = B_MN ? TN : plan.shape().tn, half_n = tn / 2;
-  const int a_bytes = A_MN ? A_BYTES : plan.shape().a_rows * KS * 2, b_bytes = half_n * KS * 2;
-  const int stage = a_bytes + b_bytes;
+  const int a_rows = A_MN ? 128 : plan.shape().a_rows;
+  const int a_bytes = a_rows * KS * 2, b_bytes = half_n * KS * 2, stage = a_bytes + b_bytes;
   const int stages = min(MAX_STAGES, S * STAGE / stage);
   const uint32_t idesc = tc::idesc_bf16(TM, tn, A_MN, B_MN);
   extern __shared__ uint8_t smem_raw[];
@@ -198,12 +200,12 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
       for (int i = pair; i < count && !*abort_flag; i += pairs) {
         const Item w = next;
         if (i + pairs < count) next = plan.item(i + pairs);   // its arithmetic under this item's waits
-        const int m0 = w.m * TM + 128 * rank, n0 = w.n * tn + half_n * rank;
+        const int m0 = (2 * w.m + rank) * a_rows, n0 = w.n * tn + half_n * rank;
         // rows beyond A are not loaded: what they multiply is never looked at
-        const bool odd_a = w.m * TM + 128 < plan.shape().M, load_a = rank == 0 || odd_a;
+        const bool odd_a = (2 * w.m + 1) * a_rows < plan.shape().M, load_a = rank == 0 || odd_a;
         const uint32_t bytes = (odd_a ? 2 : 1) * a_bytes + 2 * b_bytes;        // both CTAs' operands of a step
         for (int k = w.k0; k < w.k1; ++k) {
-          if (*abort_flag || !tc::mbar_wait(&empty[s], phase, check)) { *abort_flag = 1; break; }
+          if (!tc::mbar_wait(&empty[s], phase, check)) { *abort_flag = 1; break; }
           uint8_t* a = smem + s * stage;
           uint8_t* b = a + a_bytes;
           if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], bytes);
@@ -249,6 +251,13 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
       int s = 0, j = 0;
       uint32_t phase = 0;
       bool ok = true;
+      // operand descriptors of stage 0; the address field (16-byte units) of later
+      // stages and K steps stays within its 14 bits
+      const uint32_t base = tc::smem_u32(smem);
+      const uint64_t first_a = A_MN ? tc::sdesc(base, 8192, 1024, tc::kSwizzle128) : tc::sdesc(base, 16, 1024, tc::kSwizzle128);
+      const uint64_t first_b = B_MN ? tc::sdesc(base + a_bytes, 8192, 1024, tc::kSwizzle128)
+                                    : tc::sdesc(base + a_bytes, 16, 1024, tc::kSwizzle128);
+      uint64_t desc_a = first_a, desc_b = first_b;
       Item next = pair < count ? plan.item(pair) : Item{};
       for (int i = pair; i < count && ok; i += pairs, ++j) {
         const Item w = next;
@@ -257,22 +266,25 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
         if (*abort_flag || !tc::mbar_wait(&acc_empty[b], ((j >> 1) & 1) ^ 1, check)) { *abort_flag = 1; break; }
         tc::tc_fence_after();
         const uint32_t acc = tc::tmem_addr(tmem, 0, b * TN);
+        // One thread issues everything, so what it does per step is on the critical
+        // path of narrow tiles (0.32 us a step with an abort check and descriptors
+        // built anew, whatever the tile's size): a failed wait is the only way out,
+        // and descriptors move by constants.
         for (int k = w.k0; k < w.k1; ++k) {
-          if (*abort_flag || !tc::mbar_wait(&full[s], phase, check)) { *abort_flag = 1; ok = false; break; }
+          if (!tc::mbar_wait(&full[s], phase, check)) { *abort_flag = 1; ok = false; break; }
           tc::tc_fence_after();
-          const uint32_t ab = tc::smem_u32(smem + s * stage), bb = ab + a_bytes;
 #pragma unroll
-          for (int kk = 0; kk < KS / 16; ++kk) {
-            const uint64_t ad = A_MN ? tc::sdesc(ab + kk * 2048, 8192, 1024, tc::kSwizzle128)
-                                     : tc::sdesc(ab + kk * 32, 16, 1024, tc::kSwizzle128);
-            const uint64_t bd = B_MN ? tc::sdesc(bb + kk * 2048, 8192, 1024, tc::kSwizzle128)
-                                     : tc::sdesc(bb + kk * 32, 16, 1024, tc::kSwizzle128);
-            tc::mma_ss_pair(acc, ad, bd, idesc, (k > w.k0 || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < KS / 16; ++kk)
+            tc::mma_ss_pair(acc, desc_a + kk * ((A_MN ? 2048 : 32) >> 4), desc_b + kk * ((B_MN ? 2048 : 32) >> 4), idesc,
+                            (k > w.k0 || kk > 0) ? 1u : 0u);
           tc::mma_commit_pair(&empty[s]);
+          desc_a += stage >> 4;
+          desc_b += stage >> 4;
           if (++s == stages) {
             s = 0;
             phase ^= 1u;
+            desc_a = first_a;
+            desc_b = first_b;
           }
         }
         if (ok) tc::mma_commit_pair(&acc_full[b]);
@@ -285,7 +297,7 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
     Item next{};
     if (pair < count) {
       next = plan.item(pair);
-      epi.ready(next, next.m * TM + 128 * rank, next.n * tn, warp, lane);
+      epi.ready(next, (2 * next.m + rank) * a_rows, next.n * tn, warp, lane);
     }
     int j = 0;
     for (int i = pair; i < count; i += pairs, ++j) {
@@ -294,13 +306,13 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
       epi.take();
       if (i + pairs < count) {
         next = plan.item(i + pairs);
-        epi.ready(next, next.m * TM + 128 * rank, next.n * tn, warp, lane);
+        epi.ready(next, (2 * next.m + rank) * a_rows, next.n * tn, warp, lane);
       }
       bool have = !*abort_flag && tc::mbar_wait(&acc_full[b], (j >> 1) & 1, check);
       have = __all_sync(0xffffffffu, have);   // tcgen05.ld is warp-collective
       if (!have) { *abort_flag = 1; break; }
       tc::tc_fence_after();
-      epi.tile(tc::tmem_addr(tmem, 32 * (warp & 3), b * TN), w.m * TM + 128 * rank, w.n * tn, w, warp, lane, scratch);
+      epi.tile(tc::tmem_addr(tmem, 32 * (warp & 3), b * TN), (2 * w.m + rank) * a_rows, w.n * tn, w, warp, lane, scratch);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_cluster(acc_empty_even + 8 * b);
@@ -331,8 +343,8 @@ inline Shape shape_of(int64_t M, int64_t N, int64_t K) {
   s.nt = (int)tiles_of(N);
   s.ksteps = (int)((K + KS - 1) / KS);
   s.M = (int)M;
-  s.tn = TN;
   s.a_rows = 128;
+  s.tn = TN;
   // about as many M as N tiles among the pairs in flight: the fewest operand bytes
   // per step (4 to 32 measured alike within the noise of the power cap)
   s.group = s.mt < 8 ? s.mt : 8;

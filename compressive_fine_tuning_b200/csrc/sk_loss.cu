@@ -35,6 +35,8 @@ namespace {
 
 constexpr int64_t kExpBytes = int64_t(512) << 20;   // buffer of one chunk's exponentials
 constexpr int64_t kLossChunk = 32768;               // tokens per launch when only the loss is wanted
+constexpr int kScoreTokens = 64;                    // tokens up to which a loss alone exchanges the product's sides
+constexpr int kMinRows = 64;                        // fewest classes per CTA there
 constexpr int kMinTile = 128;                       // fewest classes per tile of a loss without gradients
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -58,6 +60,15 @@ __device__ __forceinline__ int64_t class_of(const void* target, int target64, in
     return -1;
   }
   return y;
+}
+
+// Join (maximum, sum of exponentials) pairs.  fmaxf drops a NaN maximum, but a
+// tile with a NaN logit has a NaN sum, which stays.
+__device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  const float base = top == -INFINITY ? 0.f : top;
+  s = s * expf(m - base) + s2 * expf(m2 - base);
+  m = top;
 }
 
 // ----------------------------------------------------------------------------
@@ -173,6 +184,74 @@ logit_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ C
   LogitEpi epi{&tm_e, a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.tn,
                a.store != 0, a.check, {}};
   gemm::run<0, 0, 4, 6>(&tm_h, &tm_w, gemm::Plan{a.shape}, epi, a.check);
+}
+
+// The loss alone of a few tokens: the product with its sides exchanged (M = classes,
+// N = the tokens, 32 or 64 of them), since a 256-row tile of tokens would spend
+// the tensor pipe on rows that do not exist and no longer keep up with reading W.
+// An accumulator row is then a class, so a warp turns its 32 x 32 blocks over in
+// shared memory, a lane takes one token's 32 classes, and the CTA's four warps join
+// their pairs: one (maximum, sum) per token and CTA tile of `rows` classes.
+struct ScoreEpi {
+  float2* stats;            // [CTA tiles][T]
+  float* target_logit;      // [T]
+  const void* target;
+  int target64;
+  int64_t ignore_index;
+  int T, V, rows;
+  unsigned int* check;
+
+  __device__ __forceinline__ void start(int, int, uint8_t*) {}
+  __device__ __forceinline__ void ready(const gemm::Item&, int, int, int, int) {}
+  __device__ __forceinline__ void take() {}
+  __device__ __forceinline__ void done(int) {}
+  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int, const gemm::Item&, int warp, int lane,
+                                       uint8_t* scratch) {
+    float* block = reinterpret_cast<float*>(scratch) + warp * 32 * 33;             // [class][token], padded
+    float2* pairs = reinterpret_cast<float2*>(scratch + 4 * 32 * 33 * sizeof(float));   // [warp][kScoreTokens]
+    const int c0 = m0 + 32 * warp, classes = min(32, min(rows - 32 * warp, V - c0));
+    for (int q = 0; 32 * q < T; ++q) {
+      uint32_t v[32];
+      tc::tmem_ld32(tmem + 32 * q, v);
+      tc::tmem_ld_wait();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) block[lane * 33 + j] = __uint_as_float(v[j]);
+      __syncwarp();
+      const int t = 32 * q + lane;
+      float m = -INFINITY, s = 0.f;
+      for (int c = 0; c < classes; ++c) m = fmaxf(m, block[c * 33 + lane]);
+      const float base = m == -INFINITY ? 0.f : m;
+      for (int c = 0; c < classes; ++c) s += fast_exp2((block[c * 33 + lane] - base) * kLog2e);
+      pairs[warp * kScoreTokens + t] = make_float2(m, s);
+      if (t < T) {
+        const int64_t y = class_of(target, target64, t, V, ignore_index, check);
+        if (y >= c0 && y < c0 + classes) target_logit[t] = block[(int)(y - c0) * 33 + lane];
+      }
+    }
+    tc::named_bar_sync(1, 128);
+    const int t = 32 * warp + lane;
+    if (t < T) {                                       // a CTA beyond the last class: (-inf, 0)
+      float2 p = pairs[t];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const float2 o = pairs[w * kScoreTokens + t];
+        join_stats(p.x, p.y, o.x, o.y);
+      }
+      stats[(int64_t)(m0 / rows) * T + t] = p;
+    }
+    tc::named_bar_sync(1, 128);
+  }
+};
+
+__global__ void __launch_bounds__(gemm::threads(4), 1)
+score_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h, LogitArgs a) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.shared->blocks = 0;
+    if (!a.keep_count) a.shared->count = 0;
+  }
+  ScoreEpi epi{a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.a_rows, a.check};
+  gemm::run<0, 0, 4, 6>(&tm_w, &tm_h, gemm::Plan{a.shape}, epi, a.check);
 }
 
 // ----------------------------------------------------------------------------
@@ -359,15 +438,6 @@ __global__ void __launch_bounds__(1024) count_kernel(const void* target, int tar
   }
 }
 
-// Join (maximum, sum of exponentials) pairs.  fmaxf drops a NaN maximum, but a
-// tile with a NaN logit has a NaN sum, which stays.
-__device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
-  const float top = fmaxf(m, m2);
-  const float base = top == -INFINITY ? 0.f : top;
-  s = s * expf(m - base) + s2 * expf(m2 - base);
-  m = top;
-}
-
 struct LseArgs {
   const float2* stats;
   float* nll;               // the target's logits in, the losses out
@@ -389,28 +459,29 @@ struct LseArgs {
   unsigned int* check;
 };
 
-// lse and loss of eight tokens per block: 32 thread rows walk the vocabulary's
+// lse and loss of eight tokens per block: Y thread rows walk the vocabulary's
 // tiles, then their pairs are joined by halves.
 // The loss is (maximum - l_target) + log(sum): next to lse - l_target it keeps the
 // digits of a surely predicted token, whose maximum is the target's own logit.
 // The block that finishes last sums the losses, in an order of its own, so the
 // sum does not depend on which block that is.
-__global__ void __launch_bounds__(256) lse_kernel(LseArgs a) {
-  __shared__ float2 joined[32][8];
-  __shared__ double sums[8];
+template <int Y>
+__global__ void __launch_bounds__(8 * Y) lse_kernel(LseArgs a) {
+  __shared__ float2 joined[Y][8];
+  __shared__ double sums[Y / 4];
   __shared__ bool last;
   const int t = blockIdx.x * 8 + threadIdx.x, y = threadIdx.y, tid = y * 8 + threadIdx.x;
   float m = -INFINITY, s = 0.f;
   if (t < a.T) {
 #pragma unroll 4
-    for (int i = y; i < a.tiles; i += 32) {
+    for (int i = y; i < a.tiles; i += Y) {
       const float2 p = a.stats[(int64_t)i * a.T + t];
       join_stats(m, s, p.x, p.y);
     }
   }
   joined[y][threadIdx.x] = make_float2(m, s);
 #pragma unroll
-  for (int half = 16; half > 0; half >>= 1) {
+  for (int half = Y / 2; half > 0; half >>= 1) {
     __syncthreads();
     if (y < half) {
       const float2 o = joined[y + half][threadIdx.x];
@@ -442,14 +513,14 @@ __global__ void __launch_bounds__(256) lse_kernel(LseArgs a) {
   __threadfence();
   double sum = 0.0;
 #pragma unroll 4
-  for (int64_t k = tid; k < a.all; k += 256) sum += (double)__ldcg(a.all_losses + k);
+  for (int64_t k = tid; k < a.all; k += 8 * Y) sum += (double)__ldcg(a.all_losses + k);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if ((tid & 31) == 0) sums[tid >> 5] = sum;
   __syncthreads();
   if (tid == 0) {
     double total = 0.0;
-    for (int w = 0; w < 8; ++w) total += sums[w];
+    for (int w = 0; w < Y / 4; ++w) total += sums[w];
     if (a.mean) {
       const unsigned long long n = *reinterpret_cast<volatile unsigned long long*>(&a.shared->count);
       total /= (double)(n > 0 ? n : 1);
@@ -559,7 +630,10 @@ Layout layout(int64_t T, int64_t V, int64_t d, bool dh, bool dw) {
   l.e = take(grads ? (size_t)l.chunk * l.pitch * 2 : 0);
   l.acc = take(dw && l.chunk < T ? (size_t)V * d * 4 : 0);
   l.parts = take(grads ? (size_t)(num_sms() / 2) * gemm::TM * gemm::TN * 4 : 0);
-  l.stats = take((size_t)((V + kMinTile - 1) / kMinTile) * l.chunk * 8);
+  // one pair per token and tile, the narrowest tiles that balance_tiles and balance_rows choose
+  const int64_t few = T < kScoreTokens ? T : kScoreTokens;
+  const size_t wide = (size_t)((V + kMinTile - 1) / kMinTile) * l.chunk, narrow = (size_t)(2 * ((V + 2 * kMinRows - 1) / (2 * kMinRows))) * few;
+  l.stats = take((wide > narrow ? wide : narrow) * 8);
   l.lse = take((size_t)l.chunk * 4);
   l.nll = take((size_t)l.chunk * 4);
   l.rest = take((size_t)l.chunk * 4);
@@ -587,6 +661,22 @@ void balance_tiles(gemm::Shape& s, int64_t V) {
       best = rounds * tn;
       s.tn = tn;
       s.nt = (int)nt;
+    }
+  }
+  s.split_from = s.mt * s.nt;
+}
+
+// The same for the exchanged product, whose tiles are rows of W: classes per CTA.
+void balance_rows(gemm::Shape& s, int64_t V, int64_t T) {
+  const int64_t pairs = num_sms() / 2;
+  int64_t best = 0;
+  s.tn = (int)up(T, 32);
+  for (int rows = 128; rows >= kMinRows; rows -= 8) {
+    const int64_t mt = (V + 2 * rows - 1) / (2 * rows), rounds = (mt + pairs - 1) / pairs;
+    if (best == 0 || rounds * rows < best) {
+      best = rounds * rows;
+      s.a_rows = rows;
+      s.mt = (int)mt;
     }
   }
   s.split_from = s.mt * s.nt;
@@ -637,25 +727,29 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     const int64_t T = a.T - t0 < l.chunk ? a.T - t0 : l.chunk;
     const uint16_t* H = a.H + t0 * a.d;
     const void* target = static_cast<const uint8_t*>(a.target) + t0 * (a.target64 ? 8 : 4);
-    gemm::Shape shape = gemm::shape_of(T, a.V, a.d);
-    if (!grads) {
-      balance_tiles(shape, a.V);
-      // few tokens: load their rows only, which leaves room for more stages of W
-      if (T < 128) shape.a_rows = (int)up(T, 8);
-    }
-    CUtensorMap tm_h, tm_e;
-    SK_TRY(map_rows(&tm_h, H, T, a.d, a.d, 64, shape.a_rows));
-    if (grads) SK_TRY(map_rows(&tm_e, E, T, a.V, l.pitch, 64, 32));
-    else tm_e = tm_h;                              // not used
-    CUtensorMap tm_w;
-    SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, shape.tn / 2));
+    const bool score = !grads && T <= kScoreTokens;
+    gemm::Shape shape = score ? gemm::shape_of(a.V, T, a.d) : gemm::shape_of(T, a.V, a.d);
+    if (score) balance_rows(shape, a.V, T);
+    else if (!grads) balance_tiles(shape, a.V);
+    CUtensorMap tm_h, tm_w;
+    SK_TRY(map_rows(&tm_h, H, T, a.d, a.d, 64, score ? shape.tn / 2 : 128));
+    SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, score ? shape.a_rows : shape.tn / 2));
     LogitArgs la{shape, stats, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
                  grads ? 1 : 0, shared, count_first ? 1 : 0, a.check};
-    SK_TRY(gemm::launch_pairs<4, 6>(logit_kernel, gemm::items(la.shape), s, tm_h, tm_w, tm_e, la));
+    if (score) {
+      SK_TRY(gemm::launch_pairs<4, 6>(score_kernel, gemm::items(shape), s, tm_w, tm_h, la));
+    } else {
+      CUtensorMap tm_e = tm_h;                       // used with gradients only
+      if (grads) SK_TRY(map_rows(&tm_e, E, T, a.V, l.pitch, 64, 32));
+      SK_TRY(gemm::launch_pairs<4, 6>(logit_kernel, gemm::items(shape), s, tm_h, tm_w, tm_e, la));
+    }
+    const int stat_tiles = score ? 2 * shape.mt : shape.nt;
     const bool reduce = a.reduction != SK_CE_NONE && a.loss != nullptr && t0 + T >= a.T;
-    LseArgs le{stats, nll, target, a.target64, a.ignore_index, (int)T, shape.nt, a.V, lse, losses ? losses + t0 : nullptr,
+    LseArgs le{stats, nll, target, a.target64, a.ignore_index, (int)T, stat_tiles, a.V, lse, losses ? losses + t0 : nullptr,
                shared, mean && !count_first ? 1 : 0, reduce ? a.loss : nullptr, losses, a.T, mean ? 1 : 0, a.check};
-    lse_kernel<<<(unsigned)((T + 7) / 8), dim3(8, 32), 0, s>>>(le);
+    // few tokens make few blocks: more threads in each
+    if (T <= kScoreTokens) lse_kernel<128><<<(unsigned)((T + 7) / 8), dim3(8, 128), 0, s>>>(le);
+    else lse_kernel<32><<<(unsigned)((T + 7) / 8), dim3(8, 32), 0, s>>>(le);
     SK_TRY(cudaGetLastError());
     if (!grads) continue;
     const bool each = a.reduction == SK_CE_NONE;

@@ -280,7 +280,7 @@ size_t sk_workspace_bytes(int op, int64_t n, int64_t d, int bits, int gpr, int64
   if (op == SK_OP_BWD_LUT && routed_dx_possible(n, d, T, ntask))
     return sk::dlut_tc_routed_workspace(n, d, bits, gpr, T, ntask);
   if (op == SK_OP_BWD_LUT_CKPT8 && use_tensor_cores_lut8(n, d, T, ntask))
-    return sk::lut8_tc_workspace(n, d, bits, gpr, T, ntask, ntask > 1);
+    return sk::lut8_tc_workspace(n, d, bits, gpr, T, ntask);
   return 0;
 }
 
@@ -603,10 +603,12 @@ sk_status sk_linear_bwd_lut_ckpt8(const void* packed, int bits, int gpr, int64_t
   unsigned int* check = nullptr;
   st = device_state(&check);
   if (st != SK_OK) return st;
+  // one LUT set: every token is its, whatever path the batch takes
+  if (ntask == 1) task = nullptr;
   sk::Problem p = make_problem(packed, nullptr, bits, gpr, n, d, T, task, ntask, check);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = use_tensor_cores_lut8(n, d, T, ntask)
-                      ? sk::launch_lut8_tc(p, q, scale, dY, dlut, accumulate, task != nullptr && ntask > 1, workspace, s)
+                      ? sk::launch_lut8_tc(p, q, scale, dY, dlut, accumulate, task != nullptr, workspace, s)
                       : sk::launch_lut8_simt(p, q, scale, dY, dlut, accumulate, s);
   return e == cudaSuccess ? ok() : cuda_fail(e, "LUT-gradient kernel launch");
 }

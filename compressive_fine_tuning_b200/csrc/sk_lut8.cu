@@ -418,8 +418,11 @@ Layout layout(int64_t n, int64_t d, int bits, int gpr, int64_t T, int ntask, boo
   l.dy = take(routed ? (size_t)l.rows * n * 2 : 0);
   l.x = take((size_t)l.rows * d * 2);
   l.part = take((routed ? ntask : 1) * part_floats(n, d, bits, gpr) * 4);
-  // at most one part per CTA pair in the cut round
-  l.extra = take(routed ? 0 : (size_t)(num_sms() / 2) * gemm::TM * group_slots(d / gpr, gpr) * (1 << bits) * 4);
+  // the parts of the cut round beyond each tile's first
+  gemm::Shape shape = gemm::shape_of(n, d, T);
+  gemm::split_last_round(shape);
+  const int64_t parts = (int64_t)(shape.mt * shape.nt - shape.split_from) * (shape.split - 1);
+  l.extra = take(routed ? 0 : (size_t)parts * gemm::TM * group_slots(d / gpr, gpr) * (1 << bits) * 4);
   l.total = at;
   return l;
 }
@@ -493,8 +496,12 @@ __global__ void __launch_bounds__(kBlock) lut8_simt_kernel(Problem p, const int8
 
 }  // namespace
 
-size_t lut8_tc_workspace(int64_t n, int64_t d, int bits, int gpr, int64_t T, int ntask, bool routed) {
-  return layout(n, d, bits, gpr, T, ntask, routed).total;
+size_t lut8_tc_workspace(int64_t n, int64_t d, int bits, int gpr, int64_t T, int ntask) {
+  const size_t one = layout(n, d, bits, gpr, T, ntask, false).total;
+  if (ntask == 1) return one;
+  // a call for several sets may come without task ids: then it is a call for one
+  const size_t several = layout(n, d, bits, gpr, T, ntask, true).total;
+  return one > several ? one : several;
 }
 
 cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* scale, const uint16_t* dY, float* dlut,

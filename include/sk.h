@@ -281,7 +281,8 @@ sk_status sk_linear_bwd_lut_noalloc(const void* packed, int bits, int gpr, int64
  * gradient for the values that it stands for, without a bf16 copy of X.  Shape
  * rules, task rules and errors are those of sk_linear_bwd_lut; the workspace is
  * sk_workspace_bytes(SK_OP_BWD_LUT_CKPT8, ...) bytes when that is not 0 and is
- * required then.  Deterministic, with several LUT sets too.
+ * required then.  With one LUT set every token belongs to it and task is not read.
+ * Deterministic, with several LUT sets too.
  */
 sk_status sk_ckpt8_quantize(const uint16_t* X, int64_t T, int64_t d, int8_t* q, uint8_t* scale, sk_stream_t stream);
 sk_status sk_ckpt8_dequantize(const int8_t* q, const uint8_t* scale, int64_t T, int64_t d, uint16_t* X,

@@ -184,7 +184,7 @@ def test_autograd():
     yd = y.cuda().reshape(3, 20)
     loss = sk.linear_cross_entropy(hd, wd, yd)
     alone = sk.linear_cross_entropy(hd.detach(), wd.detach(), yd)
-    assert abs(float(alone) - float(loss)) <= 2.0 ** -17 + 2.0 ** -22 * np.abs(_n(h) @ _n(w).T).max()
+    assert abs(float(alone) - float(loss.detach())) <= 2.0 ** -17 + 2.0 ** -22 * np.abs(_n(h) @ _n(w).T).max()
     one = torch.autograd.grad(loss, [hd, wd], retain_graph=True)
     kept = [t.clone() for t in one]
     two = torch.autograd.grad(loss * 4.0, [hd, wd], retain_graph=True)

@@ -56,22 +56,44 @@ struct Lut8Args {
   // [segs[2z], segs[2z] + segs[2z + 1]) (multiples of 64 apart, zero rows between);
   // nullptr for one LUT set
   const int* segs;
+  // several LUT sets whose groups are whole column tiles (`per_group` of them; else
+  // 0): a pair takes a row block through all tiles of a group, its bins stay, and
+  // dlut is written at once, without partial bins and their reduction
+  int per_group;
+  float* dlut;
+  int accumulate;
   unsigned int* check;
 };
 
-// items: set after set, each set's tiles in the product's order
+// items: set after set, each set's tiles in the product's order; or, with
+// per_group, units of (set, group, row block) whose tiles follow one another in a
+// pair's sequence
 struct Lut8Plan {
   const Lut8Args& a;
+  __device__ __forceinline__ int units() const { return a.sets * a.gpr * a.shape.mt; }
   __device__ __forceinline__ int count() const {
-    return a.segs == nullptr ? gemm::items(a.shape) : a.sets * a.shape.mt * a.shape.nt;
+    if (a.segs == nullptr) return gemm::items(a.shape);
+    const int pairs = gridDim.x >> 1;
+    if (a.per_group) return (units() + pairs - 1) / pairs * a.per_group * pairs;
+    return a.sets * a.shape.mt * a.shape.nt;
   }
   __device__ __forceinline__ const gemm::Shape& shape() const { return a.shape; }
-  __device__ __forceinline__ int set_of(int i) const { return a.segs == nullptr ? 0 : i / (a.shape.mt * a.shape.nt); }
   __device__ __forceinline__ gemm::Item item(int i) const {
     if (a.segs == nullptr) return gemm::item_at(a.shape, i);
-    const int set = set_of(i);
     gemm::Item it;
-    gemm::tile_at(a.shape, i - set * a.shape.mt * a.shape.nt, it.m, it.n);
+    int set;
+    if (a.per_group) {
+      const int pairs = gridDim.x >> 1, k = i / pairs;
+      const int unit = i - k * pairs + k / a.per_group * pairs;
+      if (unit >= units()) return gemm::Item{0, 0, 0, 0, -1};      // nothing left for this pair
+      const int sg = unit / a.shape.mt;
+      set = sg / a.gpr;
+      it.m = unit - sg * a.shape.mt;
+      it.n = (sg - set * a.gpr) * a.per_group + k % a.per_group;
+    } else {
+      set = i / (a.shape.mt * a.shape.nt);
+      gemm::tile_at(a.shape, i - set * a.shape.mt * a.shape.nt, it.m, it.n);
+    }
     it.part = set;                                     // a whole tile of this set
     it.k0 = __ldg(a.segs + 2 * set) / KS;
     it.k1 = it.k0 + (__ldg(a.segs + 2 * set + 1) + KS - 1) / KS;
@@ -154,7 +176,7 @@ struct BinEpi {
   }
   // The same for a group of both halves (`low`: the lower half's bins, the upper's
   // are 512 bytes further on): each half takes every other four bins.
-  __device__ __forceinline__ void flush_both(uint32_t low, int half, float4* out, bool write) {
+  __device__ __forceinline__ void flush_both(uint32_t low, int half, float4* out, bool write, bool add) {
     low += 4096 * half;
 #pragma unroll 1
     for (int c4 = half; c4 < K / 4; c4 += 2, low += 8192) {
@@ -170,19 +192,59 @@ struct BinEpi {
           sts<e * 1024 + 512 + k * COPY>(low, 0.f);
         });
       });
-      if (write) out[c4] = make_float4(v[0], v[1], v[2], v[3]);
+      if (write && add) {
+        const float4 o = out[c4];
+        out[c4] = make_float4(o.x + v[0], o.y + v[1], o.z + v[2], o.w + v[3]);
+      } else if (write) {
+        out[c4] = make_float4(v[0], v[1], v[2], v[3]);
+      }
     }
   }
   __device__ __forceinline__ void clear(uint32_t bins) {
     unroll<COPIES * K>([&](auto c) { sts<c * 1024>(bins, 0.f); });
   }
 
+  // the next chunk's 32 columns into the bins
+  __device__ __forceinline__ void add_chunk(uint32_t tmem, bool have, uint32_t bins) {
+    const Chunk<BITS> ch = chunks[0];
+#pragma unroll
+    for (int q = 0; q + 1 < HB; ++q) chunks[q] = chunks[q + 1];
+    uint32_t v[32];
+    if (have) {
+      tc::tmem_ld32(tmem, v);
+      tc::tmem_ld_wait();
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0u;
+    }
+    unroll<8>([&](auto e4) {
+      uint32_t at[COPIES];
+      float sum[COPIES];
+      unroll<COPIES>([&](auto k) { at[k] = bins + index_1024<BITS>(ch, 4 * e4 + k); });
+      unroll<COPIES>([&](auto k) { sum[k] = lds<k * COPY>(at[k]); });
+      unroll<COPIES>([&](auto k) { sts<k * COPY>(at[k], sum[k] + __uint_as_float(v[4 * e4 + k])); });
+    });
+  }
+
   __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, const gemm::Item& it, int warp, int lane,
                                        uint8_t* scratch) {
+    if (a.per_group && it.part < 0) return;            // a pair without a unit
     const int quad = warp & 3, half = warp >> 2;
     const int64_t row = m0 + 32 * quad + lane;
     const bool have = it.k1 > it.k0;                   // a set without tokens: zeros
     const uint32_t bins = tc::smem_u32(scratch) + 4 * (32 * warp + lane);
+    if (a.per_group) {
+#pragma unroll 1
+      for (int b = 0; b < HB; ++b) add_chunk(tmem + 128 * half + 32 * b, have, bins);
+      const int g = it.n / a.per_group;
+      if (it.n - g * a.per_group == a.per_group - 1) {
+        float* out = a.dlut + (((int64_t)it.part * a.n + row) * a.gpr + g) * K;
+        tc::named_bar_sync(1 + quad, 64);
+        flush_both(bins - 512 * half, half, reinterpret_cast<float4*>(out), row < a.n, a.accumulate != 0);
+        tc::named_bar_sync(1 + quad, 64);
+      }
+      return;
+    }
     // where this tile's partial bins go
     float* dst;
     if (a.segs == nullptr && it.part >= 0 && it.part % a.shape.split != 0) {
@@ -205,7 +267,7 @@ struct BinEpi {
       float4* out = reinterpret_cast<float4*>(dst + (g - first_g) * K);
       if (shared_g && (half ? first : last)) {
         tc::named_bar_sync(1 + quad, 64);
-        flush_both(bins - 512 * half, half, out, row < a.n);
+        flush_both(bins - 512 * half, half, out, row < a.n, false);
         tc::named_bar_sync(1 + quad, 64);
       } else {
         flush(bins, out, row < a.n);
@@ -225,24 +287,7 @@ struct BinEpi {
         finish(false);
         do { ++g; g_end += gs; } while (jc >= g_end);
       }
-      const Chunk<BITS> ch = chunks[0];
-#pragma unroll
-      for (int q = 0; q + 1 < HB; ++q) chunks[q] = chunks[q + 1];
-      uint32_t v[32];
-      if (have) {
-        tc::tmem_ld32(tmem + 128 * half + 32 * b, v);
-        tc::tmem_ld_wait();
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0u;
-      }
-      unroll<8>([&](auto e4) {
-        uint32_t at[COPIES];
-        float sum[COPIES];
-        unroll<COPIES>([&](auto k) { at[k] = bins + index_1024<BITS>(ch, 4 * e4 + k); });
-        unroll<COPIES>([&](auto k) { sum[k] = lds<k * COPY>(at[k]); });
-        unroll<COPIES>([&](auto k) { sts<k * COPY>(at[k], sum[k] + __uint_as_float(v[4 * e4 + k])); });
-      });
+      add_chunk(tmem + 128 * half + 32 * b, have, bins);
     }
   }
 };
@@ -561,13 +606,23 @@ cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* sca
     e = cudaMemsetAsync(dlut + per_set, 0, (size_t)per_set * (p.ntask - 1) * 4, s);
     if (e != cudaSuccess) return e;
   }
-  const int64_t count = routed ? (int64_t)sets * args.shape.mt * args.shape.nt : gemm::items(args.shape);
+  int64_t count = routed ? (int64_t)sets * args.shape.mt * args.shape.nt : gemm::items(args.shape);
+  if (routed && p.gs % TN == 0) {
+    // whole groups per pair while that leaves at most a tenth of the last round idle
+    const int64_t units = (int64_t)sets * p.gpr * args.shape.mt, pairs = num_sms() / 2;
+    if (10 * units >= 9 * ((units + pairs - 1) / pairs * pairs)) {
+      args.per_group = (int)(p.gs / TN);
+      args.dlut = dlut;
+      args.accumulate = accumulate;
+      count = units;
+    }
+  }
   const int64_t quads = per_set * sets / 4;
   const bool cut = args.shape.split > 1;
   auto go = [&](auto bits) {
     constexpr int B = decltype(bits)::value;
     cudaError_t err = gemm::launch_pairs<8, stages(B)>(lut8_tc_kernel<B>, count, s, tm_dy, tm_x, args);
-    if (err != cudaSuccess) return err;
+    if (err != cudaSuccess || args.per_group) return err;
     const unsigned grid = (unsigned)((quads + 255) / 256);
     if (cut) lut8_reduce_kernel<B, true><<<grid, 256, 0, s>>>(args, reinterpret_cast<float4*>(dlut), accumulate, quads);
     else lut8_reduce_kernel<B, false><<<grid, 256, 0, s>>>(args, reinterpret_cast<float4*>(dlut), accumulate, quads);

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -127,6 +128,9 @@ def _stream(device: torch.device):
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str, ndim: Optional[int] = None) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda and t.is_contiguous()
+            and (ndim is None or t.dim() == ndim)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -432,9 +436,22 @@ def _on(device: torch.device):
 
 
 def _together(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    at = first.device
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.device != at:
             raise ValueError("every tensor of a call must be on one device")
+
+
+# workspace sizes by device and shape: a step asks for the same few again and again.
+# (The LUT gradient's is not kept: SK_BWD_PATH may change it.)
+@functools.lru_cache(maxsize=256)
+def _norm_bwd_bytes(device: torch.device, T: int, d: int) -> int:
+    return int(lib.sk_layer_norm_bwd_workspace_bytes(T, d))
+
+
+@functools.lru_cache(maxsize=256)
+def _cross_entropy_bytes(device: torch.device, T: int, V: int, d: int, dh: bool, dw: bool) -> int:
+    return int(lib.sk_cross_entropy_workspace_bytes(T, V, d, int(dh), int(dw)))
 
 
 def _need_ckpt8(ck: "Ckpt8"):
@@ -558,13 +575,14 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean
     _need(dy, x.dtype, "dy", 2)
     if dy.shape != x.shape:
         raise ValueError("dy must have x's shape")
-    for t, name in ((rstd, "rstd"), (None if rms else mean, "mean")):
-        if t is None and rms and name == "mean":
-            continue
-        _need(t, torch.float32, name, 1)
-        if t.numel() != T:
-            raise ValueError(f"{name} must hold one value per row")
-    _together(x, dy, rstd, None if rms else mean)
+    if rms:
+        mean = None
+    else:
+        _need(mean, torch.float32, "mean", 1)
+    _need(rstd, torch.float32, "rstd", 1)
+    if rstd.numel() != T or (mean is not None and mean.numel() != T):
+        raise ValueError("mean and rstd must hold one value per row")
+    _together(x, dy, rstd, mean)
     dev = x.device
     with _on(dev):
         dx = torch.empty_like(x) if need_dx else None
@@ -572,10 +590,9 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean
         db = torch.empty_like(weight) if bias else None
         ws, nb = None, 0
         if need_dw or bias:
-            nb = int(lib.sk_layer_norm_bwd_workspace_bytes(T, d))
+            nb = _norm_bwd_bytes(dev, T, d)
             ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
-        _check(lib.sk_layer_norm_bwd(_ptr(dy), _ptr(x), xt, T, d, _ptr(weight), wt, None if rms else _ptr(mean),
-                                     _ptr(rstd), int(rms), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nb, _stream(dev)))
+        _check(lib.sk_layer_norm_bwd(_ptr(dy), _ptr(x), xt, T, d, _ptr(weight), wt, _ptr(mean), _ptr(rstd), int(rms), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nb, _stream(dev)))
     return dx, dw, db
 
 
@@ -675,7 +692,7 @@ def cross_entropy(H: torch.Tensor, W: torch.Tensor, target: torch.Tensor, ignore
         loss = torch.empty((T,) if red == SK_CE_NONE else (), dtype=torch.float32, device=dev) if need_loss else None
         dH = torch.empty_like(H) if need_dh else None
         dW = torch.empty_like(W) if need_dw else None
-        nb = int(lib.sk_cross_entropy_workspace_bytes(T, V, d, int(need_dh), int(need_dw)))
+        nb = _cross_entropy_bytes(dev, T, V, d, need_dh, need_dw)
         ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
         _check(lib.sk_cross_entropy(_ptr(H), _ptr(W), _ptr(target), target.element_size() * 8, T, V, d, ignore_index,
                                     red, _ptr(dloss), _ptr(loss), _ptr(dH), _ptr(dW), _ptr(ws), nb, _stream(dev)))

@@ -88,6 +88,8 @@ CASES = [
     (128, 512, 4, 4, 200, 8), (320, 1024, 3, 2, 700, 3), (64, 96, 2, 1, 5, 3), (256, 256, 4, 1, 64, 8),
     (256, 512, 4, 16, 15, 1), (256, 512, 4, 16, 16, 1), (1024, 4096, 3, 2, 17, 5), (520, 1056, 2, 33, 100, 2),
     (1024, 4096, 4, 1, 3000, 1), (2568, 2080, 4, 5, 2500, 1),
+    # groups of whole column tiles with enough (set, group, row block) units for the pairs
+    (2304, 2048, 4, 4, 300, 4), (2264, 1536, 3, 2, 333, 8), (2304, 512, 2, 2, 700, 16),
 ]
 
 

@@ -244,6 +244,99 @@ struct ScoreEpi {
   }
 };
 
+// The exchanged product with its exponentials, for a number of tokens that 256-row
+// tiles of tokens would pad by much: here a tile takes as many tokens as is best (a
+// multiple of 32).  Blocks of 32 x 32 turn over in shared memory as above, once for
+// the tile's maxima (over the CTA's 128 classes), which the warps then share, and
+// once for the exponentials: a lane writes its token's 32 classes, 64 bytes.
+struct LogitTEpi {
+  uint16_t* E;              // [T][pitch] fp16
+  int64_t pitch;
+  float2* stats;            // [CTA tiles of 128 classes][T]
+  float* target_logit;      // [T]
+  const void* target;
+  int target64;
+  int64_t ignore_index;
+  int T, V, tn;
+  unsigned int* check;
+
+  __device__ __forceinline__ void start(int, int, uint8_t*) {}
+  __device__ __forceinline__ void ready(const gemm::Item&, int, int, int, int) {}
+  __device__ __forceinline__ void take() {}
+  __device__ __forceinline__ void done(int) {}
+  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, const gemm::Item&, int warp, int lane,
+                                       uint8_t* scratch) {
+    float* block = reinterpret_cast<float*>(scratch) + warp * 32 * 33;                     // [class][token], padded
+    float* maxima = reinterpret_cast<float*>(scratch + 4 * 32 * 33 * sizeof(float));       // [warp][256 tokens]
+    float* sums = maxima + 4 * 256;
+    const int c0 = m0 + 32 * warp, classes = min(32, V - c0), tokens = min(tn, T - n0);
+    auto turn = [&](int q) {
+      uint32_t v[32];
+      tc::tmem_ld32(tmem + 32 * q, v);
+      tc::tmem_ld_wait();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) block[lane * 33 + j] = __uint_as_float(v[j]);
+      __syncwarp();
+    };
+#pragma unroll 1
+    for (int q = 0; 32 * q < tokens; ++q) {
+      turn(q);
+      float m = -INFINITY;
+      for (int c = 0; c < classes; ++c) m = fmaxf(m, block[c * 33 + lane]);
+      maxima[warp * 256 + 32 * q + lane] = m;
+    }
+    tc::named_bar_sync(1, 128);
+#pragma unroll 1
+    for (int q = 0; 32 * q < tokens; ++q) {
+      turn(q);
+      const int k = 32 * q + lane, t = n0 + k;
+      const float m = fmaxf(fmaxf(maxima[k], maxima[256 + k]), fmaxf(maxima[512 + k], maxima[768 + k]));
+      const float base = m == -INFINITY ? 0.f : m;
+      float s = 0.f;
+      uint4* out = reinterpret_cast<uint4*>(E + (int64_t)t * pitch + c0);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (8 * g >= classes) break;                  // the pitch covers whole groups of eight
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = 8 * g + 2 * i;
+          const float a = c < classes ? fast_exp2((block[c * 33 + lane] - base) * kLog2e) : 0.f;
+          const float b = c + 1 < classes ? fast_exp2((block[(c + 1) * 33 + lane] - base) * kLog2e) : 0.f;
+          s += a;
+          s += b;
+          const __half2 hh = __floats2half2_rn(a, b);
+          w[i] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        if (k < tokens) out[g] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      sums[warp * 256 + k] = s;
+      if (k < tokens) {
+        const int64_t y = class_of(target, target64, t, V, ignore_index, check);
+        if (y >= c0 && y < c0 + classes) target_logit[t] = block[(int)(y - c0) * 33 + lane];
+      }
+    }
+    tc::named_bar_sync(1, 128);
+    for (int k = 32 * warp + lane; k < tokens && m0 < V; k += 128) {
+      const float m = fmaxf(fmaxf(maxima[k], maxima[256 + k]), fmaxf(maxima[512 + k], maxima[768 + k]));
+      stats[(int64_t)(m0 / 128) * T + n0 + k] = make_float2(m, (sums[k] + sums[256 + k]) + (sums[512 + k] + sums[768 + k]));
+    }
+    tc::named_bar_sync(1, 128);
+  }
+};
+
+__global__ void __launch_bounds__(gemm::threads(4), 1)
+logit_t_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h, LogitArgs a, uint16_t* E,
+               int64_t pitch) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.shared->blocks = 0;
+    if (!a.keep_count) a.shared->count = 0;
+  }
+  LogitTEpi epi{E, pitch, a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.tn, a.check};
+  gemm::run<0, 0, 4, 6>(&tm_w, &tm_h, gemm::Plan{a.shape}, epi, a.check);
+}
+
 __global__ void __launch_bounds__(gemm::threads(4), 1)
 score_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h, LogitArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -382,6 +475,92 @@ grad_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ GradArgs a) {
   GradEpi epi{&tm_out, a.out, a.parts, a.check, {}};
   gemm::run<A_MN, 1, 4, 6>(&tm_a, &tm_b, gemm::Plan{a.shape}, epi, a.check);
+}
+
+// dH with its sides exchanged, for the same numbers of tokens: D = W^T P^T, a
+// lane of the accumulator is a column of dH.  Blocks turn over in shared memory; a
+// lane writes 32 columns of its token.
+struct GradTEpi {
+  uint16_t* out;            // bf16 [T][d]
+  const GradOut& o;         // M tokens, N columns
+  float* parts;             // [parts][256 tokens][256 columns]
+  int tn;
+  unsigned int* check;
+
+  __device__ __forceinline__ void start(int, int, uint8_t*) {}
+  __device__ __forceinline__ void ready(const gemm::Item&, int, int, int, int) {}
+  __device__ __forceinline__ void take() {}
+  __device__ __forceinline__ void done(int) {}
+  __device__ __forceinline__ void tile(uint32_t tmem, int m0, int n0, const gemm::Item& item, int warp, int lane,
+                                       uint8_t* scratch) {
+    float* block = reinterpret_cast<float*>(scratch) + warp * 32 * 33;                     // [column][token], padded
+    const int64_t c0 = m0 + 32 * warp;
+    if (c0 >= o.N) return;
+    const int tokens = (int)(o.M - n0 < tn ? o.M - n0 : tn);
+#pragma unroll 1
+    for (int q = 0; 32 * q < tokens; ++q) {
+      uint32_t v[32];
+      tc::tmem_ld32(tmem + 32 * q, v);
+      tc::tmem_ld_wait();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) block[lane * 33 + j] = __uint_as_float(v[j]);
+      __syncwarp();
+      const int k = 32 * q + lane;
+      if (k >= tokens) continue;
+      const int64_t t = n0 + k;
+      float r = 0.f;
+      const uint16_t* wrow = item.part < 0 ? o.rest.row(t, r, check) : nullptr;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (c0 + 8 * g >= o.N) break;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = block[(8 * g + e) * 33 + lane];
+        if (item.part >= 0) {
+          float4* p = reinterpret_cast<float4*>(parts + ((int64_t)item.part * 256 + k) * 256 + (m0 & 255) + 32 * warp + 8 * g);
+          p[0] = make_float4(f[0], f[1], f[2], f[3]);
+          p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+          o.finish(f, t, c0 + 8 * g, wrow, r);
+          *reinterpret_cast<uint4*>(out + t * o.N + c0 + 8 * g) =
+              make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
+                         f32x2_to_bf16x2(f[6], f[7]));
+        }
+      }
+    }
+  }
+};
+
+__global__ void __launch_bounds__(gemm::threads(4), 1)
+grad_t_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_p,
+              const __grid_constant__ GradArgs a, uint16_t* out) {
+  GradTEpi epi{out, a.out, reinterpret_cast<float*>(a.parts), a.shape.tn, a.check};
+  gemm::run<1, 0, 4, 6>(&tm_w, &tm_p, gemm::Plan{a.shape}, epi, a.check);
+}
+
+// Joins its cut tiles: block (tile, eight tokens), thread = (token, eight columns).
+__global__ void __launch_bounds__(256) join_t_kernel(const __grid_constant__ GradArgs a, uint16_t* __restrict__ out) {
+  const gemm::Shape& s = a.shape;
+  int m, n;
+  gemm::tile_at(s, s.split_from + blockIdx.x, m, n);
+  const int k = 8 * blockIdx.y + (threadIdx.x >> 5), c = 8 * (threadIdx.x & 31);
+  const int64_t t = (int64_t)n * s.tn + k, col = (int64_t)m * 256 + c;
+  if (k >= s.tn || t >= a.out.M || col >= a.out.N) return;
+  float r;
+  const uint16_t* wrow = a.out.rest.row(t, r, a.check);
+  float f[8] = {};
+  for (int q = 0; q < s.split; ++q) {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.parts) +
+                                                      (((int64_t)blockIdx.x * s.split + q) * 256 + k) * 256 + c);
+    const float4 x = p[0], y = p[1];
+    f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+    f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+  }
+  a.out.finish(f, t, col, wrow, r);
+  *reinterpret_cast<uint4*>(out + t * a.out.N + col) =
+      make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
+                 f32x2_to_bf16x2(f[6], f[7]));
 }
 
 // Joins the parts of the tiles that were cut along K, in part order: block
@@ -544,6 +723,7 @@ struct ProbArgs {
   const float* dloss;
   int dloss_each;           // dloss has one value per token
   const Shared* shared;     // divide by its count (mean), or nullptr
+  int unit_shift;           // log2 of a stats tile's width in units of eight classes (5 or 4)
   float* rest;              // [T]: P's target entry minus its bf16
   unsigned int* check;
 };
@@ -565,9 +745,9 @@ __global__ void __launch_bounds__(kProbThreads) prob_kernel(ProbArgs a) {
   const float z = a.lse[t];
   const float at_target = c * expm1f(-a.nll[t]);
   if (threadIdx.x == 0) a.rest[t] = at_target - __bfloat162float(__float2bfloat16_rn(at_target));
-  // a warp's 32 units of eight columns are one 256-column tile: one factor per warp and step
+  // a warp's 32 units of eight columns are one tile or two: one factor or two per warp and step
   for (int u = threadIdx.x; u < units; u += kProbThreads) {
-    const float f = c * __expf(a.stats[(int64_t)(u >> 5) * a.T + t].x - z);
+    const float f = c * __expf(a.stats[(int64_t)(u >> a.unit_shift) * a.T + t].x - z);
     const uint4 v = row[u];
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -682,6 +862,41 @@ void balance_rows(gemm::Shape& s, int64_t V, int64_t T) {
   s.split_from = s.mt * s.nt;
 }
 
+// Tiles of `tn` tokens on the N side.
+void token_tiles(gemm::Shape& s, int64_t T, int tn) {
+  s.tn = tn;
+  s.nt = (int)((T + tn - 1) / tn);
+  s.split_from = s.mt * s.nt;
+}
+
+// Tokens per tile of the exchanged products, or 0 when tiles of 256 tokens are as
+// good.  The pairs take the tiles (`other` times as many as there are tiles of
+// tokens) in rounds; a K step of w tokens takes 0.16 + 0.00087 w us, 0.25 at least
+// (measured from 32 to 256), one of the straight product what 256 take.  Both
+// sides at 32000 x 4096, logits and dH, us: 50 tokens 59 + 56 straight, 51 + 48
+// exchanged; 300 tokens 96 + 96 and 88 + 82; 1029 tokens at 50021 x 5120 429 + 447
+// and 415 + 395; 700 and 2100 tokens of logits within 2 %.
+int exchanged_tokens(int64_t T, int64_t other, bool cut) {
+  const int64_t pairs = num_sms() / 2;
+  auto step = [](int w) { return w < 104 ? 0.25 : 0.16 + 0.00087 * w; };
+  // a last round that is cut along K costs its share of a round
+  auto rounds = [&](int64_t tiles) {
+    const int64_t rem = tiles % pairs, split = rem ? pairs / rem : 1;
+    return (double)(tiles / pairs) + (rem == 0 ? 0.0 : cut && split >= 2 ? 1.0 / (double)(split < 8 ? split : 8) : 1.0);
+  };
+  double best = 0.95 * rounds(gemm::tiles_of(T) * other) * step(256);
+  int tn = 0;
+  for (int w = 224; w >= 32; w -= 32) {
+    const int64_t tiles = (T + w - 1) / w;
+    const double cost = rounds(tiles * other) * step(w);
+    if (cost < best && tiles * w < up(T, 256)) {
+      best = cost;
+      tn = w;
+    }
+  }
+  return tn;
+}
+
 cudaError_t launch_join(const GradArgs& a, uint16_t* out, cudaStream_t s) {
   const int cut = a.shape.mt * a.shape.nt - a.shape.split_from;
   if (cut == 0) return cudaSuccess;
@@ -728,22 +943,27 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     const uint16_t* H = a.H + t0 * a.d;
     const void* target = static_cast<const uint8_t*>(a.target) + t0 * (a.target64 ? 8 : 4);
     const bool score = !grads && T <= kScoreTokens;
-    gemm::Shape shape = score ? gemm::shape_of(a.V, T, a.d) : gemm::shape_of(T, a.V, a.d);
+    const int logit_tn = grads ? exchanged_tokens(T, gemm::tiles_of(a.V), false) : 0;
+    const bool exchanged = score || logit_tn > 0;      // M = classes, N = tokens
+    gemm::Shape shape = exchanged ? gemm::shape_of(a.V, T, a.d) : gemm::shape_of(T, a.V, a.d);
     if (score) balance_rows(shape, a.V, T);
+    else if (exchanged) token_tiles(shape, T, logit_tn);
     else if (!grads) balance_tiles(shape, a.V);
     CUtensorMap tm_h, tm_w;
-    SK_TRY(map_rows(&tm_h, H, T, a.d, a.d, 64, score ? shape.tn / 2 : 128));
-    SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, score ? shape.a_rows : shape.tn / 2));
+    SK_TRY(map_rows(&tm_h, H, T, a.d, a.d, 64, exchanged ? shape.tn / 2 : 128));
+    SK_TRY(map_rows(&tm_w, a.W, a.V, a.d, a.d, 64, exchanged ? shape.a_rows : shape.tn / 2));
     LogitArgs la{shape, stats, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
                  grads ? 1 : 0, shared, count_first ? 1 : 0, a.check};
     if (score) {
       SK_TRY(gemm::launch_pairs<4, 6>(score_kernel, gemm::items(shape), s, tm_w, tm_h, la));
+    } else if (exchanged) {
+      SK_TRY(gemm::launch_pairs<4, 6>(logit_t_kernel, gemm::items(shape), s, tm_w, tm_h, la, E, l.pitch));
     } else {
       CUtensorMap tm_e = tm_h;                       // used with gradients only
       if (grads) SK_TRY(map_rows(&tm_e, E, T, a.V, l.pitch, 64, 32));
       SK_TRY(gemm::launch_pairs<4, 6>(logit_kernel, gemm::items(shape), s, tm_h, tm_w, tm_e, la));
     }
-    const int stat_tiles = score ? 2 * shape.mt : shape.nt;
+    const int stat_tiles = score ? 2 * shape.mt : exchanged ? (int)((a.V + 127) / 128) : shape.nt;
     const bool reduce = a.reduction != SK_CE_NONE && a.loss != nullptr && t0 + T >= a.T;
     LseArgs le{stats, nll, target, a.target64, a.ignore_index, (int)T, stat_tiles, a.V, lse, losses ? losses + t0 : nullptr,
                shared, mean && !count_first ? 1 : 0, reduce ? a.loss : nullptr, losses, a.T, mean ? 1 : 0, a.check};
@@ -754,18 +974,33 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     if (!grads) continue;
     const bool each = a.reduction == SK_CE_NONE;
     ProbArgs pa{E, l.pitch, stats, lse, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
-                each && a.dloss ? a.dloss + t0 : a.dloss, each ? 1 : 0, mean ? shared : nullptr, rest, a.check};
+                each && a.dloss ? a.dloss + t0 : a.dloss, each ? 1 : 0, mean ? shared : nullptr, exchanged ? 4 : 5, rest, a.check};
     prob_kernel<<<(unsigned)T, kProbThreads, 0, s>>>(pa);
     SK_TRY(cudaGetLastError());
     if (dh) {
       CUtensorMap tm_p, tm_dh;
-      SK_TRY(map_rows(&tm_p, E, T, a.V, l.pitch, 64, 128));
-      SK_TRY(map_rows(&tm_dh, a.dH + t0 * a.d, T, a.d, a.d, 64, 32));
+      uint16_t* out = a.dH + t0 * a.d;
       GradArgs ga{gemm::shape_of(T, a.d, a.V),
                   {nullptr, 0, 1, T, a.d, {rest, a.W, target, a.target64, a.V, a.d, a.ignore_index}}, parts, a.check};
-      gemm::split_last_round(ga.shape);
-      SK_TRY(gemm::launch_pairs<4, 6>(grad_kernel<0>, gemm::items(ga.shape), s, tm_p, tm_w_mn, tm_dh, ga));
-      SK_TRY(launch_join(ga, a.dH + t0 * a.d, s));
+      const int tn = exchanged_tokens(T, gemm::tiles_of(a.d), true);
+      if (tn > 0) {
+        ga.shape = gemm::shape_of(a.d, T, a.V);
+        token_tiles(ga.shape, T, tn);
+        gemm::split_last_round(ga.shape);
+        SK_TRY(map_rows(&tm_p, E, T, a.V, l.pitch, 64, tn / 2));
+        SK_TRY(gemm::launch_pairs<4, 6>(grad_t_kernel, gemm::items(ga.shape), s, tm_w_mn, tm_p, ga, out));
+        const int cut = ga.shape.mt * ga.shape.nt - ga.shape.split_from;
+        if (cut > 0) {
+          join_t_kernel<<<dim3((unsigned)cut, (unsigned)((tn + 7) / 8)), 256, 0, s>>>(ga, out);
+          SK_TRY(cudaGetLastError());
+        }
+      } else {
+        gemm::split_last_round(ga.shape);
+        SK_TRY(map_rows(&tm_p, E, T, a.V, l.pitch, 64, 128));
+        SK_TRY(map_rows(&tm_dh, out, T, a.d, a.d, 64, 32));
+        SK_TRY(gemm::launch_pairs<4, 6>(grad_kernel<0>, gemm::items(ga.shape), s, tm_p, tm_w_mn, tm_dh, ga));
+        SK_TRY(launch_join(ga, out, s));
+      }
     }
     if (dw) {
       CUtensorMap tm_p, tm_hm;

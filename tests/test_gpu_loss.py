@@ -53,7 +53,8 @@ def _check(got, ref, lim, what):
 
 
 SHAPES = [(1, 1, 8), (1, 2, 64), (2, 255, 72), (3, 256, 64), (5, 257, 128), (127, 300, 520), (128, 1000, 64),
-          (129, 511, 200), (256, 513, 256), (257, 100, 1000), (300, 3001, 320), (64, 20001, 64), (700, 777, 96)]
+          (129, 511, 200), (256, 513, 256), (257, 100, 1000), (300, 3001, 320), (64, 20001, 64), (700, 777, 96),
+          (40, 5000, 136), (1030, 2500, 264), (600, 4001, 520), (270, 20011, 96)]
 
 
 @pytest.mark.parametrize("reduction", ["none", "mean", "sum"])

@@ -14,7 +14,8 @@ discussion (the corrected Eq. 6 and the mapping matrix M).  The LUT update
 textbook optimizer the pages leave unnamed.  The sketching stage that
 produces the index map and the first LUTs (section 2.2: calibration Gram
 matrix, weighted Lloyd's algorithm, column-by-column mapping with error
-compensation) is in ``sketching_oracle``.  Floating point is
+compensation) is in ``sketching_oracle``; the norms, checkpoints and the
+cross entropy of a fine-tuning step are in ``operators_oracle``.  Floating point is
 float64 throughout; fp16 LUT values and bf16 activations widen exactly.
 
 Parity pins: every function here is pinned by a CPU test against something

@@ -77,17 +77,18 @@ __device__ __forceinline__ void pack8(const float (&v)[8], Raw<T>& r) {
 // A team's view of a row: chunk c of member `me` of `team` holds eight columns.
 // VEC: eight consecutive ones (16-byte accesses; d % 8 == 0 and aligned rows),
 // else columns `team` apart (any d).
-template <bool VEC>
+// FULL: the team's chunks cover the row exactly, nothing to check.
+template <bool VEC, bool FULL = false>
 struct Cols {
   int me, team, d;
   __device__ __forceinline__ int col(int c, int k) const {
     return VEC ? (c * team + me) * 8 + k : (c * 8 + k) * team + me;
   }
-  __device__ __forceinline__ bool in(int c, int k) const { return col(c, VEC ? 0 : k) < d; }
+  __device__ __forceinline__ bool in(int c, int k) const { return FULL || col(c, VEC ? 0 : k) < d; }
 };
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(Raw<T>& r, const T* __restrict__ row, const Cols<VEC>& C, int c) {
+template <typename T, bool VEC, bool FULL>
+__device__ __forceinline__ void load8(Raw<T>& r, const T* __restrict__ row, const Cols<VEC, FULL>& C, int c) {
   if constexpr (VEC) {
     if (C.in(c, 0)) {
       const uint4* p = reinterpret_cast<const uint4*>(row + C.col(c, 0));
@@ -114,8 +115,8 @@ __device__ __forceinline__ void load8(Raw<T>& r, const T* __restrict__ row, cons
   }
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* __restrict__ row, const Raw<T>& r, const Cols<VEC>& C, int c) {
+template <typename T, bool VEC, bool FULL>
+__device__ __forceinline__ void store8(T* __restrict__ row, const Raw<T>& r, const Cols<VEC, FULL>& C, int c) {
   if constexpr (VEC) {
     if (C.in(c, 0)) {
       uint4* p = reinterpret_cast<uint4*>(row + C.col(c, 0));
@@ -183,9 +184,9 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormFwd a) {
   Raw<T> cur[NC], nxt[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    if (t < a.T) load8<T, VEC>(cur[c], x + t * a.d, C, c);
-    load8<WT, VEC>(w[c], static_cast<const WT*>(a.w), C, c);
-    if (a.b != nullptr) load8<WT, VEC>(b[c], static_cast<const WT*>(a.b), C, c);
+    if (t < a.T) load8<T>(cur[c], x + t * a.d, C, c);
+    load8<WT>(w[c], static_cast<const WT*>(a.w), C, c);
+    if (a.b != nullptr) load8<WT>(b[c], static_cast<const WT*>(a.b), C, c);
   }
   const float inv_d = 1.f / (float)a.d;
   // Buffers of the sums: a layer norm's two sums take turns; an RMS norm's only
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormFwd a) {
     const bool more = t + teams < a.T;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      if (more) load8<T, VEC>(nxt[c], x + (t + teams) * a.d, C, c);
+      if (more) load8<T>(nxt[c], x + (t + teams) * a.d, C, c);
     float mu = 0.f;
     if (!a.rms) {
       float s = 0.f;
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormFwd a) {
       }
       Raw<T> o;
       pack8<T>(v, o);
-      store8<T, VEC>(static_cast<T*>(a.y) + t * a.d, o, C, c);
+      store8<T>(static_cast<T*>(a.y) + t * a.d, o, C, c);
       if constexpr (CK) {
         // four neighbouring lanes hold one 32-column block (d % 32 == 0)
         uint32_t byte;
@@ -270,15 +271,15 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormBwd a) {
   auto fetch = [&](int64_t row, Raw<T>(&rx)[NC], Raw<T>(&rd)[NC], float& m, float& rs) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      load8<T, VEC>(rx[c], x + row * a.d, C, c);
-      load8<T, VEC>(rd[c], dy + row * a.d, C, c);
+      load8<T>(rx[c], x + row * a.d, C, c);
+      load8<T>(rd[c], dy + row * a.d, C, c);
     }
     m = a.rms ? 0.f : __ldg(a.mean + row);
     rs = __ldg(a.rstd + row);
   };
   if (t < a.T) fetch(t, cx, cd, mu, r);
 #pragma unroll
-  for (int c = 0; c < NC; ++c) load8<WT, VEC>(w[c], static_cast<const WT*>(a.w), C, c);
+  for (int c = 0; c < NC; ++c) load8<WT>(w[c], static_cast<const WT*>(a.w), C, c);
   if constexpr (DW) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormBwd a) {
         }
         Raw<T> o;
         pack8<T>(v, o);
-        store8<T, VEC>(static_cast<T*>(a.dx) + t * a.d, o, C, c);
+        store8<T>(static_cast<T*>(a.dx) + t * a.d, o, C, c);
       }
     }
 #pragma unroll
@@ -479,12 +480,12 @@ __device__ __forceinline__ void clear_sums(float* buf, int n) {
 }
 
 // Forward: CTA = rows 2 blockIdx.x and the next.
-template <typename T, typename WT, int MAXT, int MINB, bool RMS, bool BIAS, bool CK>
+template <typename T, typename WT, int MAXT, int MINB, bool RMS, bool BIAS, bool CK, bool FULL>
 __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_pair_kernel(NormFwd a) {
   constexpr int NC = pair_chunks<T>(), R = 2;
   __shared__ __align__(16) float buf[2][R * 32];
   const int lane = threadIdx.x & 31;
-  const Cols<true> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const Cols<true, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
   const int64_t t = (int64_t)blockIdx.x * R;
   const bool two = a.T - t >= R;
   const T* x = static_cast<const T*>(a.x) + t * a.d;
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_pair_kernel(NormFwd a) {
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      if (r == 0 || two) load8<T, true>(cur[r][c], x + r * a.d, C, c);
+      if (r == 0 || two) load8<T>(cur[r][c], x + r * a.d, C, c);
       else cur[r][c] = Raw<T>{};
     }
   clear_sums(&buf[0][0], 2 * R);
@@ -541,8 +542,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_pair_kernel(NormFwd a) {
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     Raw<WT> w, b;
-    load8<WT, true>(w, static_cast<const WT*>(a.w), C, c);
-    if constexpr (BIAS) load8<WT, true>(b, static_cast<const WT*>(a.b), C, c);
+    load8<WT>(w, static_cast<const WT*>(a.w), C, c);
+    if constexpr (BIAS) load8<WT>(b, static_cast<const WT*>(a.b), C, c);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (r > 0 && !two) break;
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_pair_kernel(NormFwd a) {
       }
       Raw<T> o;
       pack_pairs<T>(v, o);
-      store8<T, true>(static_cast<T*>(a.y) + (t + r) * a.d, o, C, c);
+      store8<T>(static_cast<T*>(a.y) + (t + r) * a.d, o, C, c);
       if constexpr (CK) {
         uint32_t byte;
         const uint2 q8 = ckpt8_quantize8(o.w, byte);
@@ -571,11 +572,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_pair_kernel(NormFwd a) {
 }
 
 // dx alone (a norm whose weights are not trained): CTA = rows 2 blockIdx.x and the next.
-template <typename T, typename WT, int MAXT, int MINB, bool RMS>
+template <typename T, typename WT, int MAXT, int MINB, bool RMS, bool FULL>
 __global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
   constexpr int NC = pair_chunks<T>(), R = 2;
   __shared__ __align__(16) float buf[2 * R * 32];
-  const Cols<true> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const Cols<true, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
   const int64_t t = (int64_t)blockIdx.x * R;
   const bool two = a.T - t >= R;
   const T* x = static_cast<const T*>(a.x) + t * a.d;
@@ -588,8 +589,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       if (there) {
-        load8<T, true>(cx[r][c], x + r * a.d, C, c);
-        load8<T, true>(cd[r][c], dy + r * a.d, C, c);
+        load8<T>(cx[r][c], x + r * a.d, C, c);
+        load8<T>(cd[r][c], dy + r * a.d, C, c);
       } else {
         cx[r][c] = cd[r][c] = Raw<T>{};
       }
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       Raw<WT> w;
-      load8<WT, true>(w, static_cast<const WT*>(a.w), C, c);
+      load8<WT>(w, static_cast<const WT*>(a.w), C, c);
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     Raw<WT> w;
-    load8<WT, true>(w, static_cast<const WT*>(a.w), C, c);
+    load8<WT>(w, static_cast<const WT*>(a.w), C, c);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (r > 0 && !two) break;
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
       }
       Raw<T> o;
       pack_pairs<T>(v, o);
-      store8<T, true>(static_cast<T*>(a.dx) + (t + r) * a.d, o, C, c);
+      store8<T>(static_cast<T*>(a.dx) + (t + r) * a.d, o, C, c);
     }
   }
 }
@@ -672,8 +673,8 @@ struct Ring {
   uint32_t row_bytes;      // a slot holds two rows of x and two of dy
 };
 
-template <typename T>
-__device__ __forceinline__ void take8(Raw<T>& r, const uint8_t* row, const Cols<true>& C, int c, bool there) {
+template <typename T, bool FULL>
+__device__ __forceinline__ void take8(Raw<T>& r, const uint8_t* row, const Cols<true, FULL>& C, int c, bool there) {
   if (there && C.in(c, 0)) {
     const uint4* p = reinterpret_cast<const uint4*>(row + (size_t)C.col(c, 0) * sizeof(T));
 #pragma unroll
@@ -687,13 +688,13 @@ __device__ __forceinline__ void take8(Raw<T>& r, const uint8_t* row, const Cols<
   }
 }
 
-template <typename T, typename WT, int MAXT, int MINB, bool RMS>
+template <typename T, typename WT, int MAXT, int MINB, bool RMS, bool FULL>
 __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_ring_kernel(NormBwd a, Ring ring) {
   constexpr int NC = 2, R = 2;
   extern __shared__ __align__(128) uint8_t rows[];           // [stages][R rows of x, R rows of dy]
   __shared__ uint64_t full[kMaxStages];
   __shared__ __align__(16) float buf[2][2 * R * 32];
-  const Cols<true> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const Cols<true, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
   const int64_t step = (int64_t)gridDim.x * R;
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_ring_kernel(NormBwd a, Ri
   f2 dw[NC][4], db[NC][4];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    load8<WT, true>(w[c], static_cast<const WT*>(a.w), C, c);
+    load8<WT>(w[c], static_cast<const WT*>(a.w), C, c);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[c][i] = db[c][i] = f2_of(0.f, 0.f);
   }
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_ring_kernel(NormBwd a, Ri
         }
         Raw<T> o;
         pack_pairs<T>(v, o);
-        store8<T, true>(static_cast<T*>(a.dx) + (t + r) * a.d, o, C, c);
+        store8<T>(static_cast<T*>(a.dx) + (t + r) * a.d, o, C, c);
       }
     }
   }
@@ -881,7 +882,7 @@ template <class Kern, class Args>
 cudaError_t launch_ring(Kern kern, unsigned grid, int threads, size_t stage_bytes, const Ring& ring, const Args& a,
                         cudaStream_t s) {
   const size_t smem = stage_bytes * ring.stages;
-  if (smem > (48 << 10)) {
+  if (smem > (32 << 10)) {               // with the kernel's own arrays it may pass the default 48 KB
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
@@ -904,11 +905,20 @@ cudaError_t fwd_shape(const NormFwd& a, cudaStream_t s) {
         kern<<<(unsigned)((a.T + 1) / 2), th, 0, s>>>(a);
         return cudaGetLastError();
       };
+      // Rows that the threads cover exactly, nothing to check: 26.7 against 29.7 us at
+      // [8192, 4096], and 30.2 against 34.3 at [4096, 5120] of a layer norm with a checkpoint.
+      // An RMS norm with a checkpoint is slower so (27.7 against 25.4 us at [4096, 5120]: the
+      // compiler moves more ahead, into registers) and keeps the checks.
+      const bool full = a.d == (int64_t)th * 8 * pair_chunks<T>();
       auto shape = [&](auto rms, auto bias) {
         constexpr bool RMS = decltype(rms)::value, BIAS = decltype(bias)::value;
-        if (th <= 128) return run(norm_fwd_pair_kernel<T, WT, 128, 5, RMS, BIAS, CK>);
-        if (th <= 256) return run(norm_fwd_pair_kernel<T, WT, 256, 2, RMS, BIAS, CK>);
-        return run(norm_fwd_pair_kernel<T, WT, 1024, 1, RMS, BIAS, CK>);
+        if constexpr (!(CK && RMS)) {
+          if (th <= 128 && full) return run(norm_fwd_pair_kernel<T, WT, 128, 5, RMS, BIAS, CK, true>);
+          if (th <= 256 && full) return run(norm_fwd_pair_kernel<T, WT, 256, 2, RMS, BIAS, CK, true>);
+        }
+        if (th <= 128) return run(norm_fwd_pair_kernel<T, WT, 128, 5, RMS, BIAS, CK, false>);
+        if (th <= 256) return run(norm_fwd_pair_kernel<T, WT, 256, 2, RMS, BIAS, CK, false>);
+        return run(norm_fwd_pair_kernel<T, WT, 1024, 1, RMS, BIAS, CK, false>);
       };
       const std::true_type yes;
       const std::false_type no;
@@ -989,8 +999,12 @@ cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
       const Ring ring{stages, (uint32_t)row};
       auto run = [&](auto rms) {
         constexpr bool RMS = decltype(rms)::value;
-        return th <= 256 ? launch_ring(norm_bwd_ring_kernel<T, WT, 256, 2, RMS>, (unsigned)parts, th, 4 * row, ring, a, s)
-                         : launch_ring(norm_bwd_ring_kernel<T, WT, 512, 1, RMS>, (unsigned)parts, th, 4 * row, ring, a, s);
+        const bool full = a.d == (int64_t)th * 16;
+        auto go = [&](auto kern) { return launch_ring(kern, (unsigned)parts, th, 4 * row, ring, a, s); };
+        if (th <= 256 && full) return go(norm_bwd_ring_kernel<T, WT, 256, 2, RMS, true>);
+        if (th <= 256) return go(norm_bwd_ring_kernel<T, WT, 256, 2, RMS, false>);
+        if (full) return go(norm_bwd_ring_kernel<T, WT, 512, 1, RMS, true>);
+        return go(norm_bwd_ring_kernel<T, WT, 512, 1, RMS, false>);
       };
       e = a.rms ? run(std::true_type()) : run(std::false_type());
       if (e != cudaSuccess) return e;
@@ -1002,9 +1016,12 @@ cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
       };
       auto shape = [&](auto rms) {
         constexpr bool RMS = decltype(rms)::value;
-        if (dx_th <= 128) return run(norm_dx_pair_kernel<T, WT, 128, 4, RMS>);
-        if (dx_th <= 256) return run(norm_dx_pair_kernel<T, WT, 256, 2, RMS>);
-        return run(norm_dx_pair_kernel<T, WT, 1024, 1, RMS>);
+        const bool full = a.d == (int64_t)dx_th * 8 * pair_chunks<T>();
+        if (dx_th <= 128 && full) return run(norm_dx_pair_kernel<T, WT, 128, 4, RMS, true>);
+        if (dx_th <= 128) return run(norm_dx_pair_kernel<T, WT, 128, 4, RMS, false>);
+        if (dx_th <= 256 && full) return run(norm_dx_pair_kernel<T, WT, 256, 2, RMS, true>);
+        if (dx_th <= 256) return run(norm_dx_pair_kernel<T, WT, 256, 2, RMS, false>);
+        return run(norm_dx_pair_kernel<T, WT, 1024, 1, RMS, false>);
       };
       return a.rms ? shape(std::true_type()) : shape(std::false_type());
     }

@@ -126,6 +126,8 @@ def test_many_rows_take_turns():
                               (3001, 4104, "bf16", "bf16", False), (1185, 1536, "fp16", "fp32", True),
                               (1184, 2056, "fp32", "fp32", False), (2367, 5120, "bf16", "bf16", True),
                               (1301, 8192, "bf16", "fp32", False), (1200, 8192, "fp32", "fp32", True),
+                              (1300, 2048, "bf16", "fp32", False), (1500, 1024, "fp16", "fp16", True),
+                              (2500, 600, "bf16", "bf16", False), (1250, 4096, "bf16", "bf16", False),
                               (1201, 9000, "bf16", "bf16", False), (1186, 17000, "fp16", "fp16", True)):
         x, w, b, dy = _case(T, d, dt, wt)
         xd, wd, bd, dyd = (t.cuda() for t in (x, w, b, dy))
@@ -137,6 +139,8 @@ def test_many_rows_take_turns():
         _check(y, ref, HALF[dt] * np.abs(ref) + K * V * (np.abs(W) * spread + np.abs(B)) + _smallest(dt), "y")
         _check(rstd, r, K * V * r * (1 + (np.abs(X).mean(1) * r) ** 2), "rstd")
         if ck is not None:
+            alone = sk.layer_norm_fwd(xd, wd, bd, 1e-5, rms)[0]
+            _check(alone, ref, HALF[dt] * np.abs(ref) + K * V * (np.abs(W) * spread + np.abs(B)) + _smallest(dt), "y alone")
             want = sk.ckpt8(y)
             assert torch.equal(ck.q, want.q) and torch.equal(ck.scale, want.scale)
         dx, dw, db = sk.layer_norm_bwd(dyd, xd, wd, mean, rstd, rms)

@@ -159,7 +159,15 @@ struct LogitEpi {
 struct Shared {
   unsigned long long count;   // tokens that take part
   unsigned int blocks;        // blocks of lse_kernel that are done
+  unsigned int dirty;         // a token that takes no part has a NaN or an infinity in its row of H
 };
+
+__device__ __forceinline__ void start_chunk(Shared* s, int keep_count) {
+  if (blockIdx.x != 0 || threadIdx.x != 0) return;
+  s->blocks = 0;
+  s->dirty = 0;
+  if (!keep_count) s->count = 0;
+}
 
 struct LogitArgs {
   gemm::Shape shape;
@@ -177,10 +185,7 @@ struct LogitArgs {
 __global__ void __launch_bounds__(gemm::threads(4), 1)
 logit_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_w,
              const __grid_constant__ CUtensorMap tm_e, LogitArgs a) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    a.shared->blocks = 0;
-    if (!a.keep_count) a.shared->count = 0;
-  }
+  start_chunk(a.shared, a.keep_count);
   LogitEpi epi{&tm_e, a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.tn,
                a.store != 0, a.check, {}};
   gemm::run<0, 0, 4, 6>(&tm_h, &tm_w, gemm::Plan{a.shape}, epi, a.check);
@@ -329,20 +334,14 @@ struct LogitTEpi {
 __global__ void __launch_bounds__(gemm::threads(4), 1)
 logit_t_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h, LogitArgs a, uint16_t* E,
                int64_t pitch) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    a.shared->blocks = 0;
-    if (!a.keep_count) a.shared->count = 0;
-  }
+  start_chunk(a.shared, a.keep_count);
   LogitTEpi epi{E, pitch, a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.tn, a.check};
   gemm::run<0, 0, 4, 6>(&tm_w, &tm_h, gemm::Plan{a.shape}, epi, a.check);
 }
 
 __global__ void __launch_bounds__(gemm::threads(4), 1)
 score_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h, LogitArgs a) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    a.shared->blocks = 0;
-    if (!a.keep_count) a.shared->count = 0;
-  }
+  start_chunk(a.shared, a.keep_count);
   ScoreEpi epi{a.stats, a.target_logit, a.target, a.target64, a.ignore_index, a.T, a.V, a.shape.a_rows, a.check};
   gemm::run<0, 0, 4, 6>(&tm_w, &tm_h, gemm::Plan{a.shape}, epi, a.check);
 }
@@ -465,6 +464,7 @@ struct GradArgs {
   gemm::Shape shape;
   GradOut out;
   float4* parts;
+  const Shared* shared;       // dW: which H to read, see clean_kernel
   unsigned int* check;
 };
 
@@ -472,9 +472,11 @@ struct GradArgs {
 template <int A_MN>
 __global__ void __launch_bounds__(gemm::threads(4), 1)
 grad_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-            const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ GradArgs a) {
+            const __grid_constant__ CUtensorMap tm_clean, const __grid_constant__ CUtensorMap tm_out,
+            const __grid_constant__ GradArgs a) {
   GradEpi epi{&tm_out, a.out, a.parts, a.check, {}};
-  gemm::run<A_MN, 1, 4, 6>(&tm_a, &tm_b, gemm::Plan{a.shape}, epi, a.check);
+  const CUtensorMap* b = A_MN && a.shared->dirty ? &tm_clean : &tm_b;
+  gemm::run<A_MN, 1, 4, 6>(&tm_a, b, gemm::Plan{a.shape}, epi, a.check);
 }
 
 // dH with its sides exchanged, for the same numbers of tokens: D = W^T P^T, a
@@ -725,10 +727,18 @@ struct ProbArgs {
   const Shared* shared;     // divide by its count (mean), or nullptr
   int unit_shift;           // log2 of a stats tile's width in units of eight classes (5 or 4)
   float* rest;              // [T]: P's target entry minus its bf16
+  const uint16_t* H;        // with dW: the tokens' rows, and whether one that takes no part is not finite
+  int64_t d;
+  unsigned int* dirty;
   unsigned int* check;
 };
 
 constexpr int kProbThreads = 256;
+
+// one of the two bf16 values has the largest exponent
+__device__ __forceinline__ bool not_finite2(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
 
 __global__ void __launch_bounds__(kProbThreads) prob_kernel(ProbArgs a) {
   const int t = blockIdx.x;
@@ -737,6 +747,15 @@ __global__ void __launch_bounds__(kProbThreads) prob_kernel(ProbArgs a) {
   const int64_t y = class_of(a.target, a.target64, t, a.V, a.ignore_index, a.check);
   if (y < 0) {
     for (int u = threadIdx.x; u < units; u += kProbThreads) row[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.H != nullptr) {
+      const uint4* h = reinterpret_cast<const uint4*>(a.H + (int64_t)t * a.d);
+      bool bad = false;
+      for (int u = threadIdx.x; u < (int)(a.d / 8); u += kProbThreads) {
+        const uint4 v = __ldg(h + u);
+        bad = bad || not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w);
+      }
+      if (bad) *a.dirty = 1;
+    }
     return;
   }
   float c = 1.f;
@@ -759,6 +778,20 @@ __global__ void __launch_bounds__(kProbThreads) prob_kernel(ProbArgs a) {
       w[q] = f32x2_to_bf16x2(lo, hi);
     }
     row[u] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// A token that takes no part has a row of zeros in P, but zero times a NaN or an
+// infinity in its row of H (padding may hold anything) would spoil all of dW.  Where
+// prob_kernel has met such a row, dW reads a copy of H with zeros in these rows.
+__global__ void __launch_bounds__(256) clean_kernel(const uint4* __restrict__ H, const void* target, int target64, int T,
+                                                    int64_t V, int64_t ignore, int64_t units, uint4* __restrict__ out,
+                                                    const Shared* shared, unsigned int* check) {
+  if (!shared->dirty) return;
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    const bool part = class_of(target, target64, t, V, ignore, check) >= 0;
+    for (int64_t u = threadIdx.x; u < units; u += 256)
+      out[t * units + u] = part ? __ldg(H + t * units + u) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -793,7 +826,7 @@ int64_t chunk_tokens(int64_t T, int64_t V, bool grads) {
 
 struct Layout {
   int64_t chunk, pitch;
-  size_t e, acc, parts, stats, lse, nll, rest, losses, shared, total;
+  size_t e, acc, parts, stats, lse, nll, rest, losses, clean, shared, total;
 };
 
 Layout layout(int64_t T, int64_t V, int64_t d, bool dh, bool dw) {
@@ -818,6 +851,7 @@ Layout layout(int64_t T, int64_t V, int64_t d, bool dh, bool dw) {
   l.nll = take((size_t)l.chunk * 4);
   l.rest = take((size_t)l.chunk * 4);
   l.losses = take((size_t)T * 4);
+  l.clean = take(dw ? (size_t)l.chunk * d * 2 : 0);
   l.shared = take(sizeof(Shared));
   l.total = at;
   return l;
@@ -974,14 +1008,15 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     if (!grads) continue;
     const bool each = a.reduction == SK_CE_NONE;
     ProbArgs pa{E, l.pitch, stats, lse, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
-                each && a.dloss ? a.dloss + t0 : a.dloss, each ? 1 : 0, mean ? shared : nullptr, exchanged ? 4 : 5, rest, a.check};
+                each && a.dloss ? a.dloss + t0 : a.dloss, each ? 1 : 0, mean ? shared : nullptr, exchanged ? 4 : 5, rest,
+                dw ? H : nullptr, a.d, &shared->dirty, a.check};
     prob_kernel<<<(unsigned)T, kProbThreads, 0, s>>>(pa);
     SK_TRY(cudaGetLastError());
     if (dh) {
       CUtensorMap tm_p, tm_dh;
       uint16_t* out = a.dH + t0 * a.d;
       GradArgs ga{gemm::shape_of(T, a.d, a.V),
-                  {nullptr, 0, 1, T, a.d, {rest, a.W, target, a.target64, a.V, a.d, a.ignore_index}}, parts, a.check};
+                  {nullptr, 0, 1, T, a.d, {rest, a.W, target, a.target64, a.V, a.d, a.ignore_index}}, parts, shared, a.check};
       const int tn = exchanged_tokens(T, gemm::tiles_of(a.d), true);
       if (tn > 0) {
         ga.shape = gemm::shape_of(a.d, T, a.V);
@@ -998,17 +1033,24 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
         gemm::split_last_round(ga.shape);
         SK_TRY(map_rows(&tm_p, E, T, a.V, l.pitch, 64, 128));
         SK_TRY(map_rows(&tm_dh, out, T, a.d, a.d, 64, 32));
-        SK_TRY(gemm::launch_pairs<4, 6>(grad_kernel<0>, gemm::items(ga.shape), s, tm_p, tm_w_mn, tm_dh, ga));
+        SK_TRY(gemm::launch_pairs<4, 6>(grad_kernel<0>, gemm::items(ga.shape), s, tm_p, tm_w_mn, tm_w_mn, tm_dh, ga));
         SK_TRY(launch_join(ga, out, s));
       }
     }
     if (dw) {
-      CUtensorMap tm_p, tm_hm;
+      CUtensorMap tm_p, tm_hm, tm_clean;
+      uint16_t* clean = reinterpret_cast<uint16_t*>(ws + l.clean);
       SK_TRY(map_rows(&tm_p, E, T, a.V, l.pitch, 64, 64));
       SK_TRY(map_rows(&tm_hm, H, T, a.d, a.d, 64, 64));
-      GradArgs ga{gemm::shape_of(a.V, a.d, T), {acc, t0 > 0 ? 1 : 0, t0 + T >= a.T ? 1 : 0, a.V, a.d, {}}, parts, a.check};
+      SK_TRY(map_rows(&tm_clean, clean, T, a.d, a.d, 64, 64));
+      const int64_t blocks = 2 * (int64_t)num_sms();
+      clean_kernel<<<(unsigned)(T < blocks ? T : blocks), 256, 0, s>>>(
+          reinterpret_cast<const uint4*>(H), target, a.target64, (int)T, a.V, a.ignore_index, a.d / 8,
+          reinterpret_cast<uint4*>(clean), shared, a.check);
+      SK_TRY(cudaGetLastError());
+      GradArgs ga{gemm::shape_of(a.V, a.d, T), {acc, t0 > 0 ? 1 : 0, t0 + T >= a.T ? 1 : 0, a.V, a.d, {}}, parts, shared, a.check};
       gemm::split_last_round(ga.shape);
-      SK_TRY(gemm::launch_pairs<4, 6>(grad_kernel<1>, gemm::items(ga.shape), s, tm_p, tm_hm, tm_dw, ga));
+      SK_TRY(gemm::launch_pairs<4, 6>(grad_kernel<1>, gemm::items(ga.shape), s, tm_p, tm_hm, tm_clean, tm_dw, ga));
       SK_TRY(launch_join(ga, a.dW, s));
     }
   }

@@ -327,8 +327,8 @@ sk_status sk_layer_norm_bwd(const void* dy, const void* x, int xtype, int64_t T,
  *   loss[t] = log(sum_v exp(l[t][v])) - l[t][target[t]].
  * target: class ids, int32 (target_bits 32) or int64 (64), device [T].  A token
  * whose id is ignore_index takes no part: its loss is 0 and its gradient is
- * zero.  Any other id outside [0, V) sets SK_CHECK_TARGET_RANGE and is treated the
- * same way.
+ * zero, whatever its row of H holds (dW stays finite over padding that is not).  Any
+ * other id outside [0, V) sets SK_CHECK_TARGET_RANGE and is treated the same way.
  * reduction: SK_CE_NONE (loss is fp32 [T]), SK_CE_MEAN (fp32 [1], the mean over the
  * tokens that take part, 0 if there are none) or SK_CE_SUM (fp32 [1]).  loss may be
  * NULL when only gradients are wanted.
@@ -339,7 +339,8 @@ sk_status sk_layer_norm_bwd(const void* dy, const void* x, int xtype, int64_t T,
  * 1 <= V < 2^24, 8 <= d < 2^20, d % 8 == 0.  T == 0: a reduced loss is 0, dW is
  * zeroed.  workspace: sk_cross_entropy_workspace_bytes(T, V, d, dH != NULL,
  * dW != NULL) bytes; with gradients it holds one chunk of tokens' exponentials
- * (512 MiB at most, or 256 tokens' if that is more).  Deterministic.
+ * (512 MiB at most, or 256 tokens' if that is more), and for dW the room of the
+ * chunk's rows of H.  Deterministic.
  *
  * sk_scale_bf16: x (bf16 [nx]) and y (bf16 [ny]; sizes multiples of 8, either may be
  * 0) times the device scalar *factor, in place, in one launch; a factor of exactly

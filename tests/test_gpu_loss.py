@@ -164,6 +164,34 @@ def test_not_finite_rows_stay_apart():
     assert torch.equal(loss[good], clean[0][good]) and torch.equal(dH[good], clean[1][good])
 
 
+@pytest.mark.parametrize("T,V,d", [(20, 600, 64), (300, 1000, 128), (520, 264, 72)])
+@pytest.mark.parametrize("reduction", ["none", "mean"])
+def test_rows_of_tokens_that_take_no_part_hold_anything(T, V, d, reduction):
+    """NaN and infinities in ignored tokens' rows (uninitialised padding) reach
+    neither the loss nor dW nor the other tokens' dH: the same numbers as with
+    zeros there."""
+    from compressive_fine_tuning_b200 import sk
+    h, w, y = _case(T, V, d, ignored=0.0)
+    out = torch.tensor([0, 7, T // 2, T - 1])
+    y[out] = -100
+    h[out] = 0.0
+    wd, yd = w.cuda(), y.cuda()
+    want = sk.cross_entropy(h.cuda(), wd, yd, reduction=reduction, need_dh=True, need_dw=True)
+    for k, bad in enumerate((float("nan"), float("inf"), -float("inf"))):
+        dirty = h.clone()
+        dirty[out[k], d - 1 - k] = bad
+        dirty[out[3]] = bad
+        got = sk.cross_entropy(dirty.cuda(), wd, yd, reduction=reduction, need_dh=True, need_dw=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(sk.cross_entropy(dirty.cuda(), wd, yd, reduction=reduction)[0],
+                           sk.cross_entropy(h.cuda(), wd, yd, reduction=reduction)[0])
+    # a class out of range is treated the same way
+    y[out[0]] = V
+    got = sk.cross_entropy(dirty.cuda(), wd, y.cuda(), reduction=reduction, need_dh=True, need_dw=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert sk.device_check() == sk.SK_CHECK_TARGET_RANGE
+
+
 def test_empty_batch():
     from compressive_fine_tuning_b200 import sk
     h = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")

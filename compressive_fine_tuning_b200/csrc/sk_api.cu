@@ -745,8 +745,14 @@ sk_status sk_cross_entropy(const uint16_t* H, const uint16_t* W, const void* tar
   const size_t lb = reduction == SK_CE_NONE ? (size_t)T * 4 : 4;
   const Buffer in[] = {{H, hb}, {W, wb}, {target, (size_t)T * (target_bits / 8)}, {dloss, lb}};
   const Buffer out[] = {{loss, lb}, {dH, hb}, {dW, wb}, {workspace, need}};
-  for (const Buffer& b : in)                    // a single value needs no more than its own alignment
-    if (b.p && !aligned16(b.p) && b.p != dloss) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  // classes, losses and their gradients are read one by one: their own size's alignment
+  // is enough (the targets of a sequence are often its ids from the second on)
+  for (const Buffer& b : in)
+    if (b.p && !aligned16(b.p) && b.p != dloss && b.p != target)
+      return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  auto aligned_to = [](const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; };
+  if (!aligned_to(target, target_bits / 8) || !aligned_to(dloss, 4) || !aligned_to(loss, 4))
+    return fail(SK_ERR_INVALID_ARG, "target, loss and dloss must be aligned to their values' size");
   for (int a = 0; a < 4; ++a) {
     if (!out[a].p) continue;
     if (!aligned16(out[a].p) && out[a].p != loss) return fail(SK_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");

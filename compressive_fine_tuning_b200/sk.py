@@ -435,6 +435,15 @@ def _on(device: torch.device):
     return torch.cuda.device(device)
 
 
+def _rows(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """Contiguous and 16-byte aligned, as the library wants it: a view into the
+    middle of a buffer may be neither."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _together(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
     at = first.device
     for t in others:
@@ -529,7 +538,7 @@ def _norm_args(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     if not isinstance(x, torch.Tensor) or x.dtype not in _NORM_TYPES:
         raise TypeError("x must be a float32, bfloat16 or float16 tensor")
     _need(x, x.dtype, "x", 2)
-    if weight.dtype not in (x.dtype, torch.float32):
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (x.dtype, torch.float32):
         raise TypeError("weight must have x's type or float32")
     _need(weight, weight.dtype, "weight", 1)
     T, d = x.shape
@@ -614,7 +623,7 @@ class LayerNormFunction(torch.autograd.Function):
     def backward(ctx, dy, *_):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dx, dw, db = layer_norm_bwd(dy.to(x.dtype).contiguous(), x, weight, mean, rstd, ctx.rms, need[2], need[0],
+        dx, dw, db = layer_norm_bwd(_rows(dy.to(x.dtype)), x, weight, mean, rstd, ctx.rms, need[2], need[0],
                                     need[1])
         return dx, dw, db, None, None, None
 
@@ -625,7 +634,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     autograd function of x, weight and bias.  With `ckpt` it returns (y, Ckpt8 of
     y's rows) for a SketchedLinear that keeps its input in 8 bits."""
     lead = x.shape[:-1]
-    rows = x if len(lead) == 1 and x.is_contiguous() else x.reshape(-1, x.shape[-1]).contiguous()
+    rows = _rows(x if len(lead) == 1 else x.reshape(-1, x.shape[-1]))
+    weight, bias = _rows(weight), _rows(bias)
     if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))):
         y, _, _, ck = layer_norm_fwd(rows, weight, bias, eps, rms, ckpt, stats=False)
     else:
@@ -745,10 +755,7 @@ def linear_cross_entropy(H: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
     lead = H.shape[:-1]
     if target.shape != lead:
         raise ValueError("target must hold one class per token")
-    if len(lead) == 1:
-        args = (H.contiguous(), W.contiguous(), target.contiguous())
-    else:
-        args = (H.reshape(-1, H.shape[-1]).contiguous(), W.contiguous(), target.reshape(-1).contiguous())
+    args = (_rows(H if len(lead) == 1 else H.reshape(-1, H.shape[-1])), _rows(W), target.reshape(-1).contiguous())
     if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
         loss = LinearCrossEntropyFunction.apply(*args, ignore_index, reduction)
     else:
@@ -817,7 +824,7 @@ class SketchedLinearCkpt8Function(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
         lut16, packed, task, q, scale = ctx.saved_tensors
-        dY = dY.to(torch.bfloat16).contiguous()
+        dY = _rows(dY.to(torch.bfloat16))
         ntask, n, gpr, _ = lut16.shape
         dX = dlut = None
         if ctx.needs_input_grad[0]:
@@ -843,7 +850,7 @@ def sketched_linear(X: torch.Tensor, lut: torch.Tensor, packed: torch.Tensor, bi
         q, scale = (None, None) if ckpt is True else ckpt
         if q is not None and tuple(q.shape) != tuple(X.shape):
             raise ValueError("the checkpoint must have X's shape")
-        return SketchedLinearCkpt8Function.apply(X.contiguous(), lut, lut16, packed, bits, task, q, scale)
+        return SketchedLinearCkpt8Function.apply(_rows(X), lut, lut16, packed, bits, task, q, scale)
     return SketchedLinearFunction.apply(X, lut, lut16, packed, bits, task)
 
 

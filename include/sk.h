@@ -336,6 +336,7 @@ sk_status sk_layer_norm_bwd(const void* dy, const void* x, int xtype, int64_t T,
  * wanted.  dloss: the gradient of the result, fp32 on the device, [T] with
  * SK_CE_NONE and [1] otherwise; NULL means ones.  Probabilities are rounded to
  * bf16 for the two gradient products, sums are fp32.
+ * target, loss and dloss need only the alignment of their own values.
  * 1 <= V < 2^24, 8 <= d < 2^20, d % 8 == 0.  T == 0: a reduced loss is 0, dW is
  * zeroed.  workspace: sk_cross_entropy_workspace_bytes(T, V, d, dH != NULL,
  * dW != NULL) bytes; with gradients it holds one chunk of tokens' exponentials

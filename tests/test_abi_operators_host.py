@@ -121,7 +121,7 @@ def ce(h=A, w=B, y=C, bits=64, T=4, V=100, d=64, ignore=-100, red=sk.SK_CE_MEAN,
     dict(bits=16), dict(T=-1), dict(T=1 << 31), dict(V=0), dict(V=1 << 24), dict(d=0), dict(d=12), dict(d=1 << 20),
     dict(red=3), dict(red=-1), dict(h=None), dict(w=None), dict(y=None), dict(ws=None), dict(nb=16), dict(ws=G + 8),
     dict(h=A + 8), dict(dH=A), dict(dW=B + 32), dict(dH=E + 2), dict(dW=E), dict(loss=A + 4), dict(ws=E), dict(ws=C),
-    dict(dloss=E + 4), dict(y=C + 8)])
+    dict(dloss=E + 4), dict(y=C + 4), dict(dloss=F + 2), dict(loss=F + 2)])
 def test_cross_entropy_arguments(kw):
     _rejected(ce(**kw))
 

@@ -164,6 +164,21 @@ def test_not_finite_rows_stay_apart():
     assert torch.equal(loss[good], clean[0][good]) and torch.equal(dH[good], clean[1][good])
 
 
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_targets_from_the_second_id_on(dtype):
+    """A sequence's targets are its ids shifted by one: a view one value further on."""
+    from compressive_fine_tuning_b200 import sk
+    h, w, y = _case(70, 500, 64)
+    ids = torch.cat([y[:1], y]).to(dtype).cuda()
+    weights = torch.rand(71, device="cuda")
+    assert ids[1:].data_ptr() % 16 and weights[1:].data_ptr() % 16
+    for red in ("none", "mean"):
+        dl = weights[1:] if red == "none" else weights[3:4]
+        got = sk.cross_entropy(h.cuda(), w.cuda(), ids[1:], reduction=red, dloss=dl, need_dh=True, need_dw=True)
+        want = sk.cross_entropy(h.cuda(), w.cuda(), y.cuda(), reduction=red, dloss=dl.clone(), need_dh=True, need_dw=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("T,V,d", [(20, 600, 64), (300, 1000, 128), (520, 264, 72)])
 @pytest.mark.parametrize("reduction", ["none", "mean"])
 def test_rows_of_tokens_that_take_no_part_hold_anything(T, V, d, reduction):

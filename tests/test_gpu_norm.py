@@ -189,6 +189,29 @@ def test_empty_batch():
     assert y.shape == (0, 64) and dx.shape == (0, 64) and not dw.any() and not db.any()
 
 
+def test_views_that_start_anywhere():
+    """Rows, weights and incoming gradients that are views into the middle of a
+    buffer, at no 16-byte boundary: the same numbers as their copies."""
+    from compressive_fine_tuning_b200 import sk
+    x, w, b, dy = _case(9, 33, "bf16", "bf16")
+    flat = torch.cat([w, b, w]).cuda()
+    ws, bs = flat[33:66].requires_grad_(), flat[66:]
+    assert ws.data_ptr() % 16 and bs.data_ptr() % 16
+    xs = x.cuda()[1:].requires_grad_()
+    assert xs.data_ptr() % 16
+    # the gradient of a concatenation is handed on as views of one buffer
+    both = torch.cat([torch.zeros(1, 33, dtype=torch.bfloat16, device="cuda"), sk.layer_norm(xs, ws, bs)])
+    got = torch.autograd.grad(both, [xs, ws], dy.cuda())
+    xc, wc = x[1:].cuda().requires_grad_(), b.cuda().requires_grad_()
+    y = sk.layer_norm(xc, wc, w.cuda())
+    want = torch.autograd.grad(y, [xc, wc], dy[1:].cuda())
+    assert torch.equal(both[1:], y) and all(torch.equal(p, q) for p, q in zip(got, want))
+    with torch.no_grad():
+        assert torch.equal(sk.layer_norm(xs, ws, bs), y)
+    with pytest.raises(sk.SketchError):
+        sk.layer_norm_fwd(xs.detach(), w.cuda())                     # the plain call refuses
+
+
 @pytest.mark.parametrize("rms", [False, True])
 def test_autograd_and_differences(rms):
     """The module's gradients against central differences of the float64 formula

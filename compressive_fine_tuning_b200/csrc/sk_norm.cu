@@ -736,7 +736,17 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_ring_kernel(NormBwd a, Ri
       off[r] = f2_of(-m, -m);
       scale[r] = f2_of(rs, rs);
     }
-    if (!tc::mbar_wait(&full[s], phase, a.check)) return;
+    if (!tc::mbar_wait(&full[s], phase, a.check)) {
+      // never leave with a copy still landing: the slots asked for ahead, each with its limit
+      for (int k = 1; k + 1 < ring.stages && t + k * step < a.T; ++k) {
+        if (++s == ring.stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+        tc::mbar_wait(&full[s], phase, a.check);
+      }
+      return;
+    }
     const uint8_t* slot = rows + (size_t)s * 2 * half_slot;
     float sums[2 * R];
 #pragma unroll

@@ -872,6 +872,8 @@ class SketchedLinear(torch.nn.Module):
     forward and the backward pass; forward(X, task, ckpt) then takes the Ckpt8 of
     X from a caller that has one (layer_norm(..., ckpt=True)) or makes its own."""
 
+    ckpt8 = False          # of modules pickled without the attribute
+
     def __init__(self, packed: torch.Tensor, lut: torch.Tensor, bits: int, in_features: int, ckpt8: bool = False):
         super().__init__()
         self.ckpt8 = ckpt8

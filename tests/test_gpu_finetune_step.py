@@ -289,3 +289,60 @@ def test_same_tensor_twice_and_refusals_on_the_device():
         sk.ckpt8(x[:, :48].contiguous())
     with pytest.raises(ValueError):
         sk.linear_cross_entropy(x, x, torch.zeros(16, dtype=torch.int64, device="cuda"), reduction="max")
+
+
+def test_offsets_beyond_32_bits():
+    """Tensors of more than 2^31 values: the last rows come out as they do alone.
+    Two roundings to bf16 lie between two ways of summing a row: 2^-7 of the value."""
+    from compressive_fine_tuning_b200 import sk
+    d, rows, last = 4096, 540000, 64
+    near = lambda a, b, slack: bool(((a.double() - b.double()).abs() <= 2.0 ** -7 * b.double().abs() + slack).all())  # noqa: E731
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.zeros(rows, d, device="cuda", dtype=torch.bfloat16)
+    assert x.numel() > 2 ** 31
+    x[-last:] = torch.randn(last, d, device="cuda", generator=g).bfloat16()
+    w = torch.rand(d, device="cuda", generator=g) + 0.5
+    tail = x[-last:].clone()
+    y, mean, rstd, ck = sk.layer_norm_fwd(x, w, w, ckpt=True)
+    ys = sk.layer_norm_fwd(tail, w, w)[0]
+    assert near(y[-last:], ys, 1e-5) and near(y[:2], w.expand(2, d), 0.0)
+    alone = sk.ckpt8(y[-last:].clone())
+    assert torch.equal(ck.q[-last:], alone.q) and torch.equal(ck.scale[-last:], alone.scale)
+    whole = sk.ckpt8(y)
+    assert torch.equal(whole.q[-last:], alone.q) and torch.equal(whole.scale, ck.scale)
+    del y
+    assert torch.equal(sk.ckpt8_dequant(ck)[-last:], sk.ckpt8_dequant(alone))
+    dy = torch.zeros_like(x)
+    dy[-last:] = torch.randn(last, d, device="cuda", generator=g).bfloat16()
+    dx, dw, db = sk.layer_norm_bwd(dy, x, w, mean, rstd)
+    # the other rows' dy is zero: the sums are the last rows'
+    sx, sw, sb = sk.layer_norm_bwd(dy[-last:].clone(), tail, w, mean[-last:].clone(), rstd[-last:].clone())
+    assert near(dx[-last:], sx, 1e-5) and not dx[:2].any()
+    assert near(dw, sw, 1e-3) and near(db, sb, 1e-3)
+    del dx, dy
+    # a LUT gradient over that many tokens: those with a gradient are the last
+    n = 64
+    idx = torch.randint(0, 4, (n, d), device="cuda", generator=g, dtype=torch.uint8)
+    packed = sk.pack(idx, 2)
+    dY = torch.zeros(rows, n, device="cuda", dtype=torch.bfloat16)
+    dY[-last:] = torch.randn(last, n, device="cuda", generator=g).bfloat16()
+    got = sk.linear_bwd_lut_ckpt8(packed, 2, 2, ck, dY)
+    want = sk.linear_bwd_lut_ckpt8(packed, 2, 2, alone, dY[-last:].clone())
+    assert near(got, want, 1e-3 * float(want.abs().max()))
+    del ck, whole, got
+    # many tokens' losses, and a head of that many values with its gradient
+    y = torch.randint(0, 40, (rows,), device="cuda", generator=g)
+    small = (torch.randn(40, d, device="cuda", generator=g) / 8).bfloat16()
+    each = sk.cross_entropy(x, small, y, reduction="none")[0]
+    assert near(each[-last:], sk.cross_entropy(tail, small, y[-last:].clone(), reduction="none")[0], 1e-4)
+    y = torch.arange(rows - last, rows, device="cuda")
+    loss, dH, dW = sk.cross_entropy(tail, x, y, need_dh=True, need_dw=True, reduction="sum")
+    # every row of the head but the last 64 is zero: their logits are 0
+    z = tail.double() @ tail.double().T
+    lse = torch.logsumexp(torch.cat([z, z.new_full((last, 1), np.log(rows - last))], 1), 1)
+    assert abs(float(loss) - float((lse - z.diagonal()).sum())) <= 1e-5 * float(lse.sum())
+    p = torch.softmax(torch.cat([z, z.new_full((last, 1), np.log(rows - last))], 1), 1)[:, :last] - torch.eye(last, device="cuda")
+    # logits of up to 4500 in fp32: an error of 2^-23 of them in the exponent
+    assert float((dW[-last:].double() - p.T @ tail.double()).abs().max()) <= 2.0 ** -6 and dW[:2].isfinite().all()
+    assert float((dH.double() - p @ tail.double()).abs().max()) <= 2.0 ** -6
+    assert sk.device_check() == 0

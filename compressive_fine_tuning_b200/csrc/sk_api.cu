@@ -142,14 +142,15 @@ bool routed_dx_possible(int64_t n, int64_t d, int64_t T, int ntask) {
   return forced == 2 || T >= kBwdTcMinT;
 }
 
-// LUT gradient from a checkpoint: the tensor cores take the bf16 gradient's
-// shapes; the token count from which the tensor cores win falls with the layer's
-// size, since their time hardly depends on a few tokens: measured 11 us against
-// 10.7 (CUDA cores) at n x d = 256 x 512 and 16 tokens, 25.3 against 25.1 at
-// 4096 x 4096 and 4, 45 against 43 at 8192 x 5120 and 1; with eight LUT sets 130
-// against 174 at 4096 x 4096 and 16, 126 against 104 at 4.
+// LUT gradient from a checkpoint: the tensor cores take any n and d (a tile beyond
+// them is zeros; on the CUDA cores every token costs a dependent load: 476 us for 962
+// tokens at n x d = 32 x 512, 13 on the tensor cores).  The token count from which the
+// tensor cores win falls with the layer's size, since their time hardly depends on a
+// few tokens: measured 11 us against 10.7 (CUDA cores) at n x d = 256 x 512 and 16
+// tokens, 25.3 against 25.1 at 4096 x 4096 and 4, 45 against 43 at 8192 x 5120 and 1;
+// with eight LUT sets 130 against 174 at 4096 x 4096 and 16, 126 against 104 at 4.
 bool use_tensor_cores_lut8(int64_t n, int64_t d, int64_t T, int ntask) {
-  if (ntask > sk::kMaxRouteTasks || n < 64 || d < 64) return false;
+  if (ntask > sk::kMaxRouteTasks) return false;
   const int forced = env_path("SK_BWD_PATH");
   if (forced == 1) return false;
   return forced == 2 || T >= 16 || T * n * d >= (int64_t(1) << (ntask > 1 ? 27 : 26));

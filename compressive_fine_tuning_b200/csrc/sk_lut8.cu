@@ -490,38 +490,43 @@ __global__ void __launch_bounds__(kBlock) lut8_simt_kernel(Problem p, const int8
   if (wid >= p.n * p.gpr) return;
   const int64_t i = wid / p.gpr, g = wid % p.gpr;
   const int64_t cpg = p.gs / 32, chunks = p.d / 32;
+  // a few tokens name few of the sets: the others get zeros (without task ids every
+  // token belongs to LUT set 0)
+  const int own = p.task != nullptr && lane < p.T ? token_task(p.task, lane, p.ntask, p.check) : -1;
   for (int tau = 0; tau < p.ntask; ++tau) {
+    const bool any = p.task == nullptr ? tau == 0 : p.T > 32 || __any_sync(0xffffffffu, own == tau);
+    if (!any) {
+      if (lane < K && !accumulate) dlut[(((int64_t)tau * p.n + i) * p.gpr + g) * K + lane] = 0.f;
+      continue;
+    }
 #pragma unroll
     for (int c = 0; c < K; ++c) bins[c][tid] = 0.f;
-    // without task ids every token belongs to LUT set 0; the other sets get zeros
-    if (p.task != nullptr || tau == 0) {
-      for (int64_t cc = lane; cc < cpg; cc += 32) {
-        const int64_t chunk = g * cpg + cc;
-        const Chunk<BITS> ch = load_chunk<BITS>(p.packed + i * p.row_bytes, chunk);
-        float G[32];
+    for (int64_t cc = lane; cc < cpg; cc += 32) {
+      const int64_t chunk = g * cpg + cc;
+      const Chunk<BITS> ch = load_chunk<BITS>(p.packed + i * p.row_bytes, chunk);
+      float G[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) G[e] = 0.f;
-        for (int64_t t = 0; t < p.T; ++t) {
-          if (p.task != nullptr && token_task(p.task, t, p.ntask, p.check) != tau) continue;
-          const uint32_t s2 = __ldg(dY + t * p.n + i);
-          const uint32_t sc = ckpt8_scale2(__ldg(scale + t * chunks + chunk));
-          const uint4* xp = reinterpret_cast<const uint4*>(q + t * p.d + chunk * 32);
+      for (int e = 0; e < 32; ++e) G[e] = 0.f;
+      for (int64_t t = 0; t < p.T; ++t) {
+        if (p.task != nullptr && token_task(p.task, t, p.ntask, p.check) != tau) continue;
+        const uint32_t s2 = __ldg(dY + t * p.n + i);
+        const uint32_t sc = ckpt8_scale2(__ldg(scale + t * chunks + chunk));
+        const uint4* xp = reinterpret_cast<const uint4*>(q + t * p.d + chunk * 32);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 v = __ldg(xp + h);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int h = 0; h < 2; ++h) {
+          const uint4 v = __ldg(xp + h);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              uint32_t w0, w1;
-              ckpt8_dequant4(w[b], sc, w0, w1);
-              fma_bf16x2_scalar(w0, s2, G[16 * h + 4 * b + 0], G[16 * h + 4 * b + 1]);
-              fma_bf16x2_scalar(w1, s2, G[16 * h + 4 * b + 2], G[16 * h + 4 * b + 3]);
-            }
+          for (int b = 0; b < 4; ++b) {
+            uint32_t w0, w1;
+            ckpt8_dequant4(w[b], sc, w0, w1);
+            fma_bf16x2_scalar(w0, s2, G[16 * h + 4 * b + 0], G[16 * h + 4 * b + 1]);
+            fma_bf16x2_scalar(w1, s2, G[16 * h + 4 * b + 2], G[16 * h + 4 * b + 3]);
           }
         }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) bins[chunk_index<BITS>(ch, e)][tid] += G[e];
       }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) bins[chunk_index<BITS>(ch, e)][tid] += G[e];
     }
     // lane partial bins -> the warp's sums (fixed shuffle tree: deterministic)
     float mine = 0.f;

@@ -119,6 +119,53 @@ def test_lut_gradient(n, d, bits, gpr, T, sets):
     assert sk.device_check() == 0
 
 
+@pytest.mark.parametrize("n,d,bits,gpr,T,sets", [(8, 32, 2, 1, 40, 1), (8, 32, 4, 1, 700, 3), (56, 1280, 4, 8, 4063, 3),
+                                                 (32, 512, 4, 8, 962, 1), (40, 64, 3, 2, 16, 8), (600, 32, 2, 1, 90, 2),
+                                                 (48, 3712, 4, 4, 17, 8), (24, 160, 3, 5, 5000, 1)])
+def test_lut_gradient_of_few_rows_or_columns(n, d, bits, gpr, T, sets):
+    """Layers smaller than one tile in either direction."""
+    from compressive_fine_tuning_b200 import sk
+    c = synth.layer_case(500 + n + T, n=n, d=d, bits=bits, gpr=gpr, T=T, ntask=sets)
+    packed, lut, X, dY, task = gc.dev_case(c)
+    ck = sk.ckpt8(X)
+    values = oo.ckpt8_values(*oo.ckpt8_quantize(c.x))
+    got = sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, task, sets)
+    ref = oracle.backward_lut(values, c.dy, c.idx, gpr, c.k, c.task, sets).reshape(got.shape)
+    assert (np.abs(got.cpu().numpy().astype(np.float64) - ref) <= _dlut_bound(c, values, c.task, sets, T).reshape(got.shape)).all()
+    assert torch.equal(got, sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, task, sets))
+    start = torch.full_like(got, 0.25)
+    acc = sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, task, sets, out=start.clone(), accumulate=True)
+    assert torch.equal(acc, start + got)
+    assert sk.device_check() == 0
+
+
+@pytest.mark.parametrize("T", [1, 9, 15])
+def test_few_tokens_of_few_of_the_sets(T):
+    """Sets that no token names are zero, or left alone when accumulating; ids out
+    of range are flagged on this path too."""
+    from compressive_fine_tuning_b200 import sk
+    n, d, bits, gpr, sets = 72, 320, 3, 5, 8
+    c = synth.layer_case(70 + T, n=n, d=d, bits=bits, gpr=gpr, T=T, ntask=sets)
+    packed, lut, X, dY, _ = gc.dev_case(c)
+    ck = sk.ckpt8(X)
+    names = np.array([5, 2, 5] * 5, dtype=np.int32)[:T]
+    task = torch.from_numpy(names).cuda()
+    values = oo.ckpt8_values(*oo.ckpt8_quantize(c.x))
+    ref = oracle.backward_lut(values, c.dy, c.idx, gpr, c.k, names, sets)
+    got = sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, task, sets)
+    # T products and additions in fp32 and at most 64 additions of the binning
+    mag = oracle.backward_lut(np.abs(values), np.abs(c.dy), c.idx, gpr, c.k, names, sets)
+    lim = ((T + 64) * 2.0 ** -23 * mag + 1e-30).reshape(got.shape)
+    assert (np.abs(got.cpu().numpy() - ref.reshape(got.shape)) <= lim).all()
+    assert not got[[0, 1, 3, 4, 6, 7]].any()
+    start = torch.full_like(got, 0.25)
+    acc = sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, task, sets, out=start.clone(), accumulate=True)
+    assert torch.equal(acc, start + got) and sk.device_check() == 0
+    task[0] = sets
+    sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, task, sets)
+    assert sk.device_check() == sk.SK_CHECK_TASK_RANGE
+
+
 def test_lut_gradient_cuda_core_path(monkeypatch):
     from compressive_fine_tuning_b200 import sk
     n, d, bits, gpr, T, sets = 72, 320, 3, 5, 150, 2

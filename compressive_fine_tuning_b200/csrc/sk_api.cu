@@ -147,13 +147,17 @@ bool routed_dx_possible(int64_t n, int64_t d, int64_t T, int ntask) {
 // tokens at n x d = 32 x 512, 13 on the tensor cores).  The token count from which the
 // tensor cores win falls with the layer's size, since their time hardly depends on a
 // few tokens: measured 11 us against 10.7 (CUDA cores) at n x d = 256 x 512 and 16
-// tokens, 25.3 against 25.1 at 4096 x 4096 and 4, 45 against 43 at 8192 x 5120 and 1;
-// with eight LUT sets 130 against 174 at 4096 x 4096 and 16, 126 against 104 at 4.
+// tokens, 25.3 against 25.1 at 4096 x 4096 and 4, 45 against 43 at 8192 x 5120 and 1.
+// With several LUT sets the tensor cores bin n d values for each, the CUDA cores only
+// for those that a token names: with three sets 63.5 against 62.6 at 4096 x 4096 and 8
+// tokens, 126 against 127 at 8192 x 5120 and 8, 18.9 against 19.8 at 1024 x 1024 and
+// 15; with eight 128 against 148 at 4096 x 4096 and 15, 127 against 90 at 8.
 bool use_tensor_cores_lut8(int64_t n, int64_t d, int64_t T, int ntask) {
   if (ntask > sk::kMaxRouteTasks) return false;
   const int forced = env_path("SK_BWD_PATH");
   if (forced == 1) return false;
-  return forced == 2 || T >= 16 || T * n * d >= (int64_t(1) << (ntask > 1 ? 27 : 26));
+  if (forced == 2 || T >= 16) return true;
+  return ntask > 1 ? T >= 6 + ntask : T * n * d >= (int64_t(1) << 26);
 }
 
 // Shape rules shared by the layer calls.

@@ -74,32 +74,62 @@ __device__ __forceinline__ void pack8(const float (&v)[8], Raw<T>& r) {
   }
 }
 
-// A team's view of a row: chunk c of member `me` of `team` holds eight columns.
-// VEC: eight consecutive ones (16-byte accesses; d % 8 == 0 and aligned rows),
-// else columns `team` apart (any d).
+// A team's view of a row: chunk c of member `me` of `team` holds eight columns, in
+// groups of V consecutive ones (V = 8, 4, 2 or 1, a divisor of d, so that a group is
+// aligned in every row and inside or outside it as a whole); the chunk's groups are
+// team * V columns apart.
 // FULL: the team's chunks cover the row exactly, nothing to check.
-template <bool VEC, bool FULL = false>
+template <int V, bool FULL = false>
 struct Cols {
   int me, team, d;
   __device__ __forceinline__ int col(int c, int k) const {
-    return VEC ? (c * team + me) * 8 + k : (c * 8 + k) * team + me;
+    return ((c * (8 / V) + k / V) * team + me) * V + k % V;
   }
-  __device__ __forceinline__ bool in(int c, int k) const { return FULL || col(c, VEC ? 0 : k) < d; }
+  __device__ __forceinline__ bool in(int c, int k) const { return FULL || col(c, k / V * V) < d; }
 };
 
-template <typename T, bool VEC, bool FULL>
-__device__ __forceinline__ void load8(Raw<T>& r, const T* __restrict__ row, const Cols<VEC, FULL>& C, int c) {
-  if constexpr (VEC) {
-    if (C.in(c, 0)) {
-      const uint4* p = reinterpret_cast<const uint4*>(row + C.col(c, 0));
+// N 32-bit words (2 or a multiple of 4, 1 for a store), aligned to their size up to 16 bytes
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t* w, const void* p) {
+  if constexpr (N == 2) {
+    const uint2 v = __ldg(static_cast<const uint2*>(p));
+    w[0] = v.x; w[1] = v.y;
+  } else {
 #pragma unroll
-      for (int q = 0; q < Raw<T>::NW / 4; ++q) {
-        const uint4 v = __ldg(p + q);
-        r.w[4 * q] = v.x; r.w[4 * q + 1] = v.y; r.w[4 * q + 2] = v.z; r.w[4 * q + 3] = v.w;
+    for (int q = 0; q < N / 4; ++q) {
+      const uint4 v = __ldg(static_cast<const uint4*>(p) + q);
+      w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
+  if constexpr (N == 1) {
+    *static_cast<uint32_t*>(p) = w[0];
+  } else if constexpr (N == 2) {
+    *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) static_cast<uint4*>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  }
+}
+
+template <typename T, int V, bool FULL>
+__device__ __forceinline__ void load8(Raw<T>& r, const T* __restrict__ row, const Cols<V, FULL>& C, int c) {
+  if constexpr (V > 1 && V * sizeof(T) == 4) {
+#pragma unroll
+    for (int g = 0; g < 8 / V; ++g)
+      r.w[g] = C.in(c, g * V) ? __ldg(reinterpret_cast<const uint32_t*>(row + C.col(c, g * V))) : 0u;
+  } else if constexpr (V > 1) {
+    constexpr int N = V * (int)sizeof(T) / 4;
+#pragma unroll
+    for (int g = 0; g < 8 / V; ++g) {
+      if (C.in(c, g * V)) {
+        load_words<N>(r.w + g * N, row + C.col(c, g * V));
+      } else {
+#pragma unroll
+        for (int q = 0; q < N; ++q) r.w[g * N + q] = 0u;
       }
-    } else {
-#pragma unroll
-      for (int q = 0; q < Raw<T>::NW; ++q) r.w[q] = 0u;
     }
   } else {
     uint32_t b[8];
@@ -115,24 +145,19 @@ __device__ __forceinline__ void load8(Raw<T>& r, const T* __restrict__ row, cons
   }
 }
 
-template <typename T, bool VEC, bool FULL>
-__device__ __forceinline__ void store8(T* __restrict__ row, const Raw<T>& r, const Cols<VEC, FULL>& C, int c) {
-  if constexpr (VEC) {
-    if (C.in(c, 0)) {
-      uint4* p = reinterpret_cast<uint4*>(row + C.col(c, 0));
+template <typename T, int V, bool FULL>
+__device__ __forceinline__ void store8(T* __restrict__ row, const Raw<T>& r, const Cols<V, FULL>& C, int c) {
+  if constexpr (V > 1) {
+    constexpr int N = V * (int)sizeof(T) / 4;
 #pragma unroll
-      for (int q = 0; q < Raw<T>::NW / 4; ++q)
-        p[q] = make_uint4(r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
-    }
+    for (int g = 0; g < 8 / V; ++g)
+      if (C.in(c, g * V)) store_words<N>(row + C.col(c, g * V), r.w + g * N);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       if (!C.in(c, k)) continue;
-      if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<uint32_t*>(row)[C.col(c, k)] = r.w[k];
-      } else {
-        reinterpret_cast<uint16_t*>(row)[C.col(c, k)] = (uint16_t)(r.w[k >> 1] >> (16 * (k & 1)));
-      }
+      if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(row)[C.col(c, k)] = r.w[k];
+      else reinterpret_cast<uint16_t*>(row)[C.col(c, k)] = (uint16_t)(r.w[k >> 1] >> (16 * (k & 1)));
     }
   }
 }
@@ -172,11 +197,11 @@ __device__ __forceinline__ float2 team_sum2(float2 v, float2* buf) {
 // forward
 // ----------------------------------------------------------------------------
 
-template <typename T, typename WT, int NC, int MAXT, bool VEC, bool WARP, bool CK>
+template <typename T, typename WT, int NC, int MAXT, int V, bool WARP, bool CK>
 __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormFwd a) {
   __shared__ float buf[2][32];
   const int lane = threadIdx.x & 31;
-  const Cols<VEC> C{WARP ? lane : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, (int)a.d};
+  const Cols<V> C{WARP ? lane : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, (int)a.d};
   const int64_t teams = WARP ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
   int64_t t = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   const T* x = static_cast<const T*>(a.x);
@@ -254,12 +279,12 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormFwd a) {
 
 // DW: also accumulate dw and db over the team's rows and write them as partial
 // row blockIdx.x of a.part ([parts][2][d]); else dx alone.
-template <typename T, typename WT, int NC, int MAXT, bool VEC, bool WARP, bool DW>
+template <typename T, typename WT, int NC, int MAXT, int V, bool WARP, bool DW>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormBwd a) {
   extern __shared__ float wpart[];                 // WARP with DW: [warps][2][NC * 256]
   __shared__ float2 buf[2][32];
   const int lane = threadIdx.x & 31;
-  const Cols<VEC> C{WARP ? lane : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, (int)a.d};
+  const Cols<V> C{WARP ? lane : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, (int)a.d};
   const int64_t teams = WARP ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
   int64_t t = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   const T* x = static_cast<const T*>(a.x);
@@ -485,7 +510,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_pair_kernel(NormFwd a) {
   constexpr int NC = pair_chunks<T>(), R = 2;
   __shared__ __align__(16) float buf[2][R * 32];
   const int lane = threadIdx.x & 31;
-  const Cols<true, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const Cols<8, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
   const int64_t t = (int64_t)blockIdx.x * R;
   const bool two = a.T - t >= R;
   const T* x = static_cast<const T*>(a.x) + t * a.d;
@@ -576,7 +601,7 @@ template <typename T, typename WT, int MAXT, int MINB, bool RMS, bool FULL>
 __global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
   constexpr int NC = pair_chunks<T>(), R = 2;
   __shared__ __align__(16) float buf[2 * R * 32];
-  const Cols<true, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const Cols<8, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
   const int64_t t = (int64_t)blockIdx.x * R;
   const bool two = a.T - t >= R;
   const T* x = static_cast<const T*>(a.x) + t * a.d;
@@ -674,7 +699,7 @@ struct Ring {
 };
 
 template <typename T, bool FULL>
-__device__ __forceinline__ void take8(Raw<T>& r, const uint8_t* row, const Cols<true, FULL>& C, int c, bool there) {
+__device__ __forceinline__ void take8(Raw<T>& r, const uint8_t* row, const Cols<8, FULL>& C, int c, bool there) {
   if (there && C.in(c, 0)) {
     const uint4* p = reinterpret_cast<const uint4*>(row + (size_t)C.col(c, 0) * sizeof(T));
 #pragma unroll
@@ -694,7 +719,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_ring_kernel(NormBwd a, Ri
   extern __shared__ __align__(128) uint8_t rows[];           // [stages][R rows of x, R rows of dy]
   __shared__ uint64_t full[kMaxStages];
   __shared__ __align__(16) float buf[2][2 * R * 32];
-  const Cols<true, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const Cols<8, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
   const int64_t step = (int64_t)gridDim.x * R;
@@ -880,6 +905,17 @@ cudaError_t by_types(int xt, int wt, F f) {
   return wt == SK_F32 ? f(__half(), float()) : f(__half(), __half());
 }
 
+// Columns per access: the base pointers are 16-byte aligned, a row starts at a
+// multiple of d values.  Single 16-bit values against pairs: 38.8 against 19.7 us
+// forward at [2037, 4782].
+template <class F>
+cudaError_t by_width(int64_t d, F f) {
+  if (d % 8 == 0) return f(std::integral_constant<int, 8>());
+  if (d % 4 == 0) return f(std::integral_constant<int, 4>());
+  if (d % 2 == 0) return f(std::integral_constant<int, 2>());
+  return f(std::integral_constant<int, 1>());
+}
+
 // Shared memory of the ring: four stages where `ctas` CTAs of an SM have room for
 // them, two at least (0: no room, the register kernels take such rows).
 int ring_stages(size_t stage_bytes, int ctas) {
@@ -905,10 +941,10 @@ cudaError_t launch_ring(Kern kern, unsigned grid, int threads, size_t stage_byte
 // (one row of 8192: 2.4 against 3.6 us).
 bool pairs_of_rows(int64_t T, int64_t d) { return d > 512 && T >= 8 * (int64_t)num_sms(); }
 
-template <typename T, typename WT, bool VEC, bool CK>
+template <typename T, typename WT, int V, bool CK>
 cudaError_t fwd_shape(const NormFwd& a, cudaStream_t s) {
   const int64_t sms = num_sms();
-  if constexpr (VEC) {
+  if constexpr (V == 8) {
     const int th = team_threads(a.d, pair_chunks<T>());
     if (th <= 1024 && pairs_of_rows(a.T, a.d)) {
       auto run = [&](auto kern) {
@@ -941,27 +977,26 @@ cudaError_t fwd_shape(const NormFwd& a, cudaStream_t s) {
     kern<<<(unsigned)grid, threads, 0, s>>>(a);
     return cudaGetLastError();
   };
-  if (a.d <= 256) return go(norm_fwd_kernel<T, WT, 1, 128, VEC, true, CK>, 128, kWarpTeams, 16);
-  if (a.d <= 512) return go(norm_fwd_kernel<T, WT, 2, 128, VEC, true, CK>, 128, kWarpTeams, 8);
+  if (a.d <= 256) return go(norm_fwd_kernel<T, WT, 1, 128, V, true, CK>, 128, kWarpTeams, 16);
+  if (a.d <= 512) return go(norm_fwd_kernel<T, WT, 2, 128, V, true, CK>, 128, kWarpTeams, 8);
   if (a.d <= 16384) {
     const int th = team_threads(a.d, 2);
-    if (th <= 256) return go(norm_fwd_kernel<T, WT, 2, 256, VEC, false, CK>, th, 1, 768 / th);
-    if (th <= 512) return go(norm_fwd_kernel<T, WT, 2, 512, VEC, false, CK>, th, 1, 1024 / th);
-    return go(norm_fwd_kernel<T, WT, 2, 1024, VEC, false, CK>, th, 1, 1);
+    if (th <= 256) return go(norm_fwd_kernel<T, WT, 2, 256, V, false, CK>, th, 1, 768 / th);
+    if (th <= 512) return go(norm_fwd_kernel<T, WT, 2, 512, V, false, CK>, th, 1, 1024 / th);
+    return go(norm_fwd_kernel<T, WT, 2, 1024, V, false, CK>, th, 1, 1);
   }
-  return go(norm_fwd_kernel<T, WT, 4, 1024, VEC, false, CK>, team_threads(a.d, 4), 1, 1);
+  return go(norm_fwd_kernel<T, WT, 4, 1024, V, false, CK>, team_threads(a.d, 4), 1, 1);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormFwd& a, cudaStream_t s) {
-  const bool vec = a.d % 8 == 0;       // the rows are 16-byte aligned then (the base pointers are)
   return by_types(a.xtype, a.wtype, [&](auto xt, auto wt) {
     using T = decltype(xt);
     using WT = decltype(wt);
-    if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value)
-      if (a.q != nullptr) return fwd_shape<T, WT, true, true>(a, s);
-    return vec ? fwd_shape<T, WT, true, false>(a, s) : fwd_shape<T, WT, false, false>(a, s);
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      if (a.q != nullptr) return fwd_shape<T, WT, 8, true>(a, s);
+    return by_width(a.d, [&](auto v) { return fwd_shape<T, WT, decltype(v)::value, false>(a, s); });
   });
 }
 
@@ -991,7 +1026,7 @@ int norm_bwd_parts(int64_t T, int64_t d) {
 
 namespace {
 
-template <typename T, typename WT, bool VEC>
+template <typename T, typename WT, int V>
 cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
   const bool dw = a.dw != nullptr || a.db != nullptr;
   const int parts = norm_bwd_parts(a.T, a.d);
@@ -999,7 +1034,7 @@ cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
   cudaError_t e;
   auto check = [&] { return cudaGetLastError(); };
   bool done = false;                   // dx and, up to kFusedDw, the partials of dw and db
-  if constexpr (VEC) {
+  if constexpr (V == 8) {
     const int th = team_threads(a.d, 2);
     const int ctas = th <= 512 ? 512 / th : 1;
     const size_t row = (size_t)a.d * sizeof(T);
@@ -1039,13 +1074,13 @@ cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
   if (done) {
   } else if (dw && a.d <= kFusedDw) {
     if (a.d <= 256)
-      norm_bwd_kernel<T, WT, 1, 128, VEC, true, true><<<parts, 128, kWarpTeams * 2 * 256 * 4, s>>>(a);
+      norm_bwd_kernel<T, WT, 1, 128, V, true, true><<<parts, 128, kWarpTeams * 2 * 256 * 4, s>>>(a);
     else if (a.d <= 512)
-      norm_bwd_kernel<T, WT, 2, 128, VEC, true, true><<<parts, 128, kWarpTeams * 2 * 512 * 4, s>>>(a);
+      norm_bwd_kernel<T, WT, 2, 128, V, true, true><<<parts, 128, kWarpTeams * 2 * 512 * 4, s>>>(a);
     else if (team_threads(a.d, 2) <= 256)
-      norm_bwd_kernel<T, WT, 2, 256, VEC, false, true><<<parts, team_threads(a.d, 2), 0, s>>>(a);
+      norm_bwd_kernel<T, WT, 2, 256, V, false, true><<<parts, team_threads(a.d, 2), 0, s>>>(a);
     else
-      norm_bwd_kernel<T, WT, 2, 512, VEC, false, true><<<parts, team_threads(a.d, 2), 0, s>>>(a);
+      norm_bwd_kernel<T, WT, 2, 512, V, false, true><<<parts, team_threads(a.d, 2), 0, s>>>(a);
     e = check();
     if (e != cudaSuccess) return e;
   } else {
@@ -1053,17 +1088,17 @@ cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
       if (a.d <= 512) {
         int64_t grid = (a.T + kWarpTeams - 1) / kWarpTeams;
         if (grid > sms * 8) grid = sms * 8;
-        norm_bwd_kernel<T, WT, 2, 128, VEC, true, false><<<(unsigned)grid, 128, 0, s>>>(a);
+        norm_bwd_kernel<T, WT, 2, 128, V, true, false><<<(unsigned)grid, 128, 0, s>>>(a);
       } else if (a.d <= 16384) {
         const int th = team_threads(a.d, 2);
         const int64_t per_sm = th < 768 ? 768 / th : 1;
         const unsigned grid = (unsigned)(a.T < sms * per_sm ? a.T : sms * per_sm);
-        if (th <= 256) norm_bwd_kernel<T, WT, 2, 256, VEC, false, false><<<grid, th, 0, s>>>(a);
-        else if (th <= 512) norm_bwd_kernel<T, WT, 2, 512, VEC, false, false><<<grid, th, 0, s>>>(a);
-        else norm_bwd_kernel<T, WT, 2, 1024, VEC, false, false><<<grid, th, 0, s>>>(a);
+        if (th <= 256) norm_bwd_kernel<T, WT, 2, 256, V, false, false><<<grid, th, 0, s>>>(a);
+        else if (th <= 512) norm_bwd_kernel<T, WT, 2, 512, V, false, false><<<grid, th, 0, s>>>(a);
+        else norm_bwd_kernel<T, WT, 2, 1024, V, false, false><<<grid, th, 0, s>>>(a);
       } else {
         const unsigned grid = (unsigned)(a.T < sms ? a.T : sms);
-        norm_bwd_kernel<T, WT, 4, 1024, VEC, false, false><<<grid, team_threads(a.d, 4), 0, s>>>(a);
+        norm_bwd_kernel<T, WT, 4, 1024, V, false, false><<<grid, team_threads(a.d, 4), 0, s>>>(a);
       }
       e = check();
       if (e != cudaSuccess) return e;
@@ -1081,11 +1116,10 @@ cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_norm_bwd(const NormBwd& a, cudaStream_t s) {
-  const bool vec = a.d % 8 == 0;
   return by_types(a.xtype, a.wtype, [&](auto xt, auto wt) {
     using T = decltype(xt);
     using WT = decltype(wt);
-    return vec ? bwd_shape<T, WT, true>(a, s) : bwd_shape<T, WT, false>(a, s);
+    return by_width(a.d, [&](auto v) { return bwd_shape<T, WT, decltype(v)::value>(a, s); });
   });
 }
 

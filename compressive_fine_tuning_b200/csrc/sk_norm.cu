@@ -78,14 +78,14 @@ __device__ __forceinline__ void pack8(const float (&v)[8], Raw<T>& r) {
 // groups of V consecutive ones (V = 8, 4, 2 or 1, a divisor of d, so that a group is
 // aligned in every row and inside or outside it as a whole); the chunk's groups are
 // team * V columns apart.
-// FULL: the team's chunks cover the row exactly, nothing to check.
-template <int V, bool FULL = false>
+// SAFE: the first so many chunks lie inside the row, nothing to check.
+template <int V, int SAFE = 0>
 struct Cols {
   int me, team, d;
   __device__ __forceinline__ int col(int c, int k) const {
     return ((c * (8 / V) + k / V) * team + me) * V + k % V;
   }
-  __device__ __forceinline__ bool in(int c, int k) const { return FULL || col(c, k / V * V) < d; }
+  __device__ __forceinline__ bool in(int c, int k) const { return c < SAFE || col(c, k / V * V) < d; }
 };
 
 // N 32-bit words (2 or a multiple of 4, 1 for a store), aligned to their size up to 16 bytes
@@ -114,8 +114,8 @@ __device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
   }
 }
 
-template <typename T, int V, bool FULL>
-__device__ __forceinline__ void load8(Raw<T>& r, const T* __restrict__ row, const Cols<V, FULL>& C, int c) {
+template <typename T, int V, int SAFE>
+__device__ __forceinline__ void load8(Raw<T>& r, const T* __restrict__ row, const Cols<V, SAFE>& C, int c) {
   if constexpr (V > 1 && V * sizeof(T) == 4) {
 #pragma unroll
     for (int g = 0; g < 8 / V; ++g)
@@ -145,8 +145,8 @@ __device__ __forceinline__ void load8(Raw<T>& r, const T* __restrict__ row, cons
   }
 }
 
-template <typename T, int V, bool FULL>
-__device__ __forceinline__ void store8(T* __restrict__ row, const Raw<T>& r, const Cols<V, FULL>& C, int c) {
+template <typename T, int V, int SAFE>
+__device__ __forceinline__ void store8(T* __restrict__ row, const Raw<T>& r, const Cols<V, SAFE>& C, int c) {
   if constexpr (V > 1) {
     constexpr int N = V * (int)sizeof(T) / 4;
 #pragma unroll
@@ -458,6 +458,10 @@ __device__ __forceinline__ void pack_pairs(const f2 (&v)[4], Raw<T>& r) {
 template <typename T>
 __host__ __device__ constexpr int pair_chunks() { return sizeof(T) == 2 ? 4 : 2; }
 
+// FULL kernels take rows that their threads cover exactly.  In the others half of a
+// thread's chunks are inside the row all the same, since team_threads takes no more
+// threads than d > 512 columns need.
+
 // Sums of N = 2 or 4 values over the CTA, in every thread.  Within a warp the lanes
 // share the values out as they halve: N - 1 + (5 - log2 N) shuffles.  buf: [N][32]
 // floats, written again only after a later sum's barrier.
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_pair_kernel(NormFwd a) {
   constexpr int NC = pair_chunks<T>(), R = 2;
   __shared__ __align__(16) float buf[2][R * 32];
   const int lane = threadIdx.x & 31;
-  const Cols<8, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const Cols<8, FULL ? NC : NC / 2> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
   const int64_t t = (int64_t)blockIdx.x * R;
   const bool two = a.T - t >= R;
   const T* x = static_cast<const T*>(a.x) + t * a.d;
@@ -601,7 +605,7 @@ template <typename T, typename WT, int MAXT, int MINB, bool RMS, bool FULL>
 __global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
   constexpr int NC = pair_chunks<T>(), R = 2;
   __shared__ __align__(16) float buf[2 * R * 32];
-  const Cols<8, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const Cols<8, FULL ? NC : NC / 2> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
   const int64_t t = (int64_t)blockIdx.x * R;
   const bool two = a.T - t >= R;
   const T* x = static_cast<const T*>(a.x) + t * a.d;
@@ -698,8 +702,8 @@ struct Ring {
   uint32_t row_bytes;      // a slot holds two rows of x and two of dy
 };
 
-template <typename T, bool FULL>
-__device__ __forceinline__ void take8(Raw<T>& r, const uint8_t* row, const Cols<8, FULL>& C, int c, bool there) {
+template <typename T, int SAFE>
+__device__ __forceinline__ void take8(Raw<T>& r, const uint8_t* row, const Cols<8, SAFE>& C, int c, bool there) {
   if (there && C.in(c, 0)) {
     const uint4* p = reinterpret_cast<const uint4*>(row + (size_t)C.col(c, 0) * sizeof(T));
 #pragma unroll
@@ -719,7 +723,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_ring_kernel(NormBwd a, Ri
   extern __shared__ __align__(128) uint8_t rows[];           // [stages][R rows of x, R rows of dy]
   __shared__ uint64_t full[kMaxStages];
   __shared__ __align__(16) float buf[2][2 * R * 32];
-  const Cols<8, FULL> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
+  const Cols<8, FULL ? NC : NC / 2> C{(int)threadIdx.x, (int)blockDim.x, (int)a.d};
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
   const int64_t step = (int64_t)gridDim.x * R;
@@ -1066,6 +1070,9 @@ cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
         if (dx_th <= 128) return run(norm_dx_pair_kernel<T, WT, 128, 4, RMS, false>);
         if (dx_th <= 256 && full) return run(norm_dx_pair_kernel<T, WT, 256, 2, RMS, true>);
         if (dx_th <= 256) return run(norm_dx_pair_kernel<T, WT, 256, 2, RMS, false>);
+        // 128 registers: at 64 dx spills (79 against 44 us at [2048, 16384] bf16), while the
+        // forward pass gains more from a second CTA (26 against 34 us)
+        if (dx_th <= 512) return run(norm_dx_pair_kernel<T, WT, 512, 1, RMS, false>);
         return run(norm_dx_pair_kernel<T, WT, 1024, 1, RMS, false>);
       };
       return a.rms ? shape(std::true_type()) : shape(std::false_type());

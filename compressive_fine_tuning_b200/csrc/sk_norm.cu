@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
 // read from there for the sums and again for dx, which leaves the registers to the
 // accumulators.  A slot is asked for again after the next pair's barrier, by which
 // every thread is done with it.  At [8192, 4096] bf16 (31 us for its traffic at
-// the copy rate): one row at a time in registers 47-52 us, pairs from the ring 41 us.
+// the copy rate): one row at a time in registers 47-52 us, pairs from the ring 43 us.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                ::"r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(tc::smem_u32(bar))

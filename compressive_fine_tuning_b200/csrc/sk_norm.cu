@@ -193,12 +193,21 @@ __device__ __forceinline__ float2 team_sum2(float2 v, float2* buf) {
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
+// CTAs per SM to leave registers for.  Single 16-bit values take many registers for
+// their addresses when left alone: one or two CTAs fit, and [4096, 4095] bf16 takes 52
+// + 70 us forward and backward, against 40 + 43 at `threads` per SM.  (Single fp32
+// values spill then, 4.9 against 10.2 us backward at [1111, 1001].)
+template <typename T, int V>
+constexpr int few_ctas(int maxt, int threads) {
+  return V == 1 && sizeof(T) == 2 && maxt <= 256 ? threads / maxt : 1;
+}
+
 // ----------------------------------------------------------------------------
 // forward
 // ----------------------------------------------------------------------------
 
 template <typename T, typename WT, int NC, int MAXT, int V, bool WARP, bool CK>
-__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormFwd a) {
+__global__ void __launch_bounds__(MAXT, few_ctas<T, V>(MAXT, 768)) norm_fwd_kernel(NormFwd a) {
   __shared__ float buf[2][32];
   const int lane = threadIdx.x & 31;
   const Cols<V> C{WARP ? lane : (int)threadIdx.x, WARP ? 32 : (int)blockDim.x, (int)a.d};
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormFwd a) {
 // DW: also accumulate dw and db over the team's rows and write them as partial
 // row blockIdx.x of a.part ([parts][2][d]); else dx alone.
 template <typename T, typename WT, int NC, int MAXT, int V, bool WARP, bool DW>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormBwd a) {
+__global__ void __launch_bounds__(MAXT, few_ctas<T, V>(MAXT, 512)) norm_bwd_kernel(NormBwd a) {
   extern __shared__ float wpart[];                 // WARP with DW: [warps][2][NC * 256]
   __shared__ float2 buf[2][32];
   const int lane = threadIdx.x & 31;

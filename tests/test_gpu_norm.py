@@ -58,8 +58,9 @@ def _smallest(dt):
 SHAPES = [(1, 1), (3, 2), (2, 31), (5, 32), (9, 100), (130, 256), (17, 257), (40, 512), (33, 513), (300, 1001),
           (8, 1024), (1000, 768), (7, 4096), (1, 8192), (70, 8192), (3, 8200), (5, 12001), (2, 16384), (3, 20000),
           (2, 32768),
-          # rows aligned to two or four values only
-          (9, 6), (70, 36), (33, 602), (21, 4092), (4, 4782), (3, 12004), (2, 18002)]
+          # rows that start anywhere: first and last chunks in part, and lengths around the limits
+          (9, 6), (70, 36), (33, 602), (21, 4092), (4, 4782), (3, 12004), (2, 18002), (70, 249), (90, 255), (40, 505),
+          (37, 511), (9, 8185), (5, 8191), (12, 16383), (9, 32761), (3, 32767)]
 
 
 @pytest.mark.parametrize("dt,wt", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp16", "fp32"),
@@ -130,7 +131,10 @@ def test_many_rows_take_turns():
                               (1301, 8192, "bf16", "fp32", False), (1200, 8192, "fp32", "fp32", True),
                               (1300, 2048, "bf16", "fp32", False), (1500, 1024, "fp16", "fp16", True),
                               (2500, 600, "bf16", "bf16", False), (1300, 1034, "bf16", "fp32", False),
-                              (1200, 2052, "fp16", "fp16", True), (1250, 4096, "bf16", "bf16", False),
+                              (1200, 2052, "fp16", "fp16", True), (5003, 251, "bf16", "fp32", False),
+                              (5003, 509, "fp16", "fp16", True), (2503, 1021, "bf16", "bf16", False),
+                              (1500, 4095, "bf16", "fp32", False), (703, 8187, "fp32", "fp32", False),
+                              (605, 9001, "bf16", "bf16", True), (310, 20003, "bf16", "fp32", False), (1250, 4096, "bf16", "bf16", False),
                               (1201, 9000, "bf16", "bf16", False), (1186, 17000, "fp16", "fp16", True)):
         x, w, b, dy = _case(T, d, dt, wt)
         xd, wd, bd, dyd = (t.cuda() for t in (x, w, b, dy))

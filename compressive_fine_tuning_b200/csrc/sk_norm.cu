@@ -199,7 +199,7 @@ __device__ __forceinline__ float2 team_sum2(float2 v, float2* buf) {
 // values spill then, 4.9 against 10.2 us backward at [1111, 1001].)
 template <typename T, int V>
 constexpr int few_ctas(int maxt, int threads) {
-  return V == 1 && sizeof(T) == 2 && maxt <= 256 ? threads / maxt : 1;
+  return V == 1 && sizeof(T) == 2 && maxt <= 256 ? threads / maxt : 0;     // 0: left to the compiler
 }
 
 // ----------------------------------------------------------------------------

@@ -697,7 +697,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_dx_pair_kernel(NormBwd a) {
 // read from there for the sums and again for dx, which leaves the registers to the
 // accumulators.  A slot is asked for again after the next pair's barrier, by which
 // every thread is done with it.  At [8192, 4096] bf16 (31 us for its traffic at
-// the copy rate): one row at a time in registers 47-52 us, pairs from the ring 43 us.
+// the copy rate): one row at a time in registers 47-52 us, pairs from the ring 43 us,
+// and 38 with the rows' statistics asked for a pair ahead too.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                ::"r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(tc::smem_u32(bar))
@@ -764,16 +765,26 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_ring_kernel(NormBwd a, Ri
   const float inv_d = 1.f / (float)a.d;
   int s = 0, before = ring.stages - 1, parity = 0;
   uint32_t phase = 0;
+  // the next pair's statistics, asked for a pair ahead as well
+  float mean[R], rstd[R];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool there = row + r < a.T;
+      mean[r] = RMS || !there ? 0.f : __ldg(a.mean + row + r);
+      rstd[r] = there ? __ldg(a.rstd + row + r) : 0.f;
+    }
+  };
+  fetch(t);
   for (; t < a.T; t += step, parity ^= 1) {
     const bool two = a.T - t >= R;
     f2 off[R], scale[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool there = r == 0 || two;
-      const float m = RMS || !there ? 0.f : __ldg(a.mean + t + r), rs = there ? __ldg(a.rstd + t + r) : 0.f;
-      off[r] = f2_of(-m, -m);
-      scale[r] = f2_of(rs, rs);
+      off[r] = f2_of(-mean[r], -mean[r]);
+      scale[r] = f2_of(rstd[r], rstd[r]);
     }
+    fetch(t + step);
     if (!tc::mbar_wait(&full[s], phase, a.check)) {
       // never leave with a copy still landing: the slots asked for ahead, each with its limit
       for (int k = 1; k + 1 < ring.stages && t + k * step < a.T; ++k) {

@@ -888,26 +888,32 @@ __global__ void __launch_bounds__(256) norm_dwdb_kernel(NormBwd a) {
   part[a.d + col] = db;
 }
 
-// dw (blockIdx.y == 0) and db (1): 32 columns per block, partial rows y, y + 16,
-// ... per thread row, then the sixteen sums in order.
-template <typename WT>
+// dw (blockIdx.y == 0) and db (1): X columns per block, partial rows y, y + 512 / X,
+// ... per thread row, joined in a fixed order.  It is bound by the latency of a
+// thread's loads, and by the number of blocks: 32 columns (a line) take 4.1 us after
+// [8192, 4096] and 7.0 after [16384, 1024], where 64 blocks add 1184 rows; eight (a
+// sector) 6.7 and 3.9.
+template <typename WT, int X>
 __global__ void __launch_bounds__(512) norm_reduce_kernel(const float* __restrict__ part, int parts, int64_t d, WT* dw,
                                                           WT* db) {
-  __shared__ float sums[16][33];
+  __shared__ float sums[16][X + 1];
   WT* out = blockIdx.y ? db : dw;
   if (out == nullptr) return;
-  const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  const int x = threadIdx.x % X, y = threadIdx.x / X, lane = threadIdx.x & 31;
+  const int64_t col = (int64_t)blockIdx.x * X + x;
   float s = 0.f;
   if (col < d) {
 #pragma unroll 8
-    for (int p = threadIdx.y; p < parts; p += 16) s += part[(int64_t)p * 2 * d + blockIdx.y * d + col];
+    for (int p = y; p < parts; p += 512 / X) s += part[(int64_t)p * 2 * d + blockIdx.y * d + col];
   }
-  sums[threadIdx.y][threadIdx.x] = s;
+#pragma unroll
+  for (int off = X; off < 32; off *= 2) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (lane < X) sums[threadIdx.x >> 5][x] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && col < d) {
+  if (threadIdx.x < X && col < d) {
     float total = 0.f;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) total += sums[q][threadIdx.x];
+    for (int q = 0; q < 16; ++q) total += sums[q][x];
     out[col] = round_to<WT>(total);
   }
 }
@@ -1135,8 +1141,11 @@ cudaError_t bwd_shape(const NormBwd& a, cudaStream_t s) {
     e = check();
     if (e != cudaSuccess) return e;
   }
-  norm_reduce_kernel<WT><<<dim3((unsigned)((a.d + 31) / 32), 2), dim3(32, 16), 0, s>>>(
-      a.part, parts, a.d, static_cast<WT*>(a.dw), static_cast<WT*>(a.db));
+  WT *out_w = static_cast<WT*>(a.dw), *out_b = static_cast<WT*>(a.db);
+  if (a.d < 16 * sms && parts >= 320)          // lines would make fewer blocks than SMs, with many rows each
+    norm_reduce_kernel<WT, 8><<<dim3((unsigned)((a.d + 7) / 8), 2), 512, 0, s>>>(a.part, parts, a.d, out_w, out_b);
+  else
+    norm_reduce_kernel<WT, 32><<<dim3((unsigned)((a.d + 31) / 32), 2), 512, 0, s>>>(a.part, parts, a.d, out_w, out_b);
   return check();
 }
 

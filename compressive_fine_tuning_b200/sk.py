@@ -466,6 +466,10 @@ def _refuse_tangent(*tensors: Optional[torch.Tensor]) -> None:
         raise NotImplementedError("the backward passes of this library have no forward-mode derivative")
 
 
+def _capturing(t: torch.Tensor) -> bool:
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 # workspace sizes by device and shape: a step asks for the same few again and again.
 # (The LUT gradient's is not kept: SK_BWD_PATH may change it.)
 @functools.lru_cache(maxsize=256)
@@ -734,7 +738,9 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
     and the backward pass scales them in place by the incoming gradient, which a
     factor of 1 leaves alone.  They are handed out once; a second backward pass
     over a retained graph computes them again, as does reduction "none", whose
-    gradient needs every token's factor."""
+    gradient needs every token's factor.  So does a backward pass that is captured
+    into a CUDA graph without its forward pass: its replays would scale the same
+    buffers again and again."""
 
     @staticmethod
     def forward(ctx, H, W, target, ignore_index, reduction):
@@ -744,6 +750,7 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         ctx.save_for_backward(H, W, target)
         ctx.args = (ignore_index, reduction)
         ctx.ready = (dH, dW) if now else None
+        ctx.captured = _capturing(H)
         return loss
 
     @staticmethod
@@ -753,7 +760,7 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         H, W, target = ctx.saved_tensors
         dh, dw = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
         g = g.to(torch.float32).contiguous()
-        if ctx.ready is None:
+        if ctx.ready is None or _capturing(H) != ctx.captured:
             _, dH, dW = cross_entropy(H, W, target, *ctx.args, dloss=g, need_loss=False, need_dh=dh, need_dw=dw)
             return dH, dW, None, None, None
         dH, dW = ctx.ready

@@ -20,6 +20,7 @@ constexpr int TM = 256, TN = 256, KS = 64;
 constexpr int A_BYTES = 128 * KS * 2, B_BYTES = 128 * KS * 2, STAGE = A_BYTES + B_BYTES;
 constexpr int SLAB = 32 * 128;                    // one warp's output slab: 32 rows x 128 bytes
 constexpr int TMEM_COLS = 512;
+constexpr int kVoteBar = 8;                       // named barriers of a team's common decision
 
 // S full stages of operands; the rest of the CTA's shared memory is the epilogue's.
 // Narrower tiles have smaller stages, and more of them in the same memory.  (An MMA
@@ -132,7 +133,10 @@ struct Plan {
   __device__ __forceinline__ Item item(int i) const { return item_at(s, i); }
 };
 
-// Epi: struct with, for every epilogue warp,
+// Epi: struct with
+//   static constexpr int kTeam
+// the number of warps that meet at barriers in tile() (named ones below kVoteBar): 1 if
+// none do, 2 for the warps w and w + 4, or all; and, for every epilogue warp,
 //   void start(int warp, int lane, uint8_t* scratch)
 // once, and for every item
 //   void ready(const Item&, int m0, int n0, int warp, int lane)
@@ -309,7 +313,11 @@ __device__ __forceinline__ void run(const CUtensorMap* tm_a, const CUtensorMap* 
         epi.ready(next, (2 * next.m + rank) * a_rows, next.n * tn, warp, lane);
       }
       bool have = !*abort_flag && tc::mbar_wait(&acc_full[b], (j >> 1) & 1, check);
-      have = __all_sync(0xffffffffu, have);   // tcgen05.ld is warp-collective
+      // tcgen05.ld is warp-collective, and a warp that went on alone would wait at the
+      // tile's barriers forever: the warps that meet there give up together.  (All eight
+      // where pairs meet: up to 2 us of 81 with 1000 tokens of three LUT sets at 4096 x 4096.)
+      if constexpr (Epi::kTeam == 1) have = __all_sync(0xffffffffu, have);
+      else have = tc::named_bar_and(kVoteBar + (Epi::kTeam == 2 ? warp & 3 : 0), 32 * Epi::kTeam, have);
       if (!have) { *abort_flag = 1; break; }
       tc::tc_fence_after();
       epi.tile(tc::tmem_addr(tmem, 32 * (warp & 3), b * TN), (2 * w.m + rank) * a_rows, w.n * tn, w, warp, lane, scratch);

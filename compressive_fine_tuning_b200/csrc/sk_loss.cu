@@ -82,6 +82,7 @@ __device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s
 // ----------------------------------------------------------------------------
 
 struct LogitEpi {
+  static constexpr int kTeam = 1;
   const CUtensorMap* tm_e;
   float2* stats;            // [tiles of V][T]: (maximum, sum of exp(l - maximum))
   float* target_logit;      // [T]
@@ -204,6 +205,7 @@ logit_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ C
 // shared memory, a lane takes one token's 32 classes, and the CTA's four warps join
 // their pairs: one (maximum, sum) per token and CTA tile of `rows` classes.
 struct ScoreEpi {
+  static constexpr int kTeam = 4;
   float2* stats;            // [CTA tiles][T]
   float* target_logit;      // [T]
   const void* target;
@@ -261,6 +263,7 @@ struct ScoreEpi {
 // the tile's maxima (over the CTA's 128 classes), which the warps then share, and
 // once for the exponentials: a lane writes its token's 32 classes, 64 bytes.
 struct LogitTEpi {
+  static constexpr int kTeam = 4;
   uint16_t* E;              // [T][pitch] fp16
   int64_t pitch;
   float2* stats;            // [CTA tiles of 128 classes][T]
@@ -416,6 +419,7 @@ struct GradOut {
 };
 
 struct GradEpi {
+  static constexpr int kTeam = 1;
   const CUtensorMap* tm_out;
   const GradOut& o;
   float4* parts;            // [parts][2 CTAs][64 groups of 4 columns][128 rows]
@@ -489,6 +493,7 @@ grad_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
 // lane of the accumulator is a column of dH.  Blocks turn over in shared memory; a
 // lane writes 32 columns of its token.
 struct GradTEpi {
+  static constexpr int kTeam = 1;
   uint16_t* out;            // bf16 [T][d]
   const GradOut& o;         // M tokens, N columns
   float* parts;             // [parts][256 tokens][256 columns]

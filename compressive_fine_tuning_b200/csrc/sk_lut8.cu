@@ -138,6 +138,7 @@ __device__ __forceinline__ void unroll(F f) {
 // halves' border is written by the lower half with both halves' sums.
 template <int BITS>
 struct BinEpi {
+  static constexpr int kTeam = 2;                    // the two warps of a row meet at a group's flush
   static constexpr int K = 1 << BITS, HB = TN / 64;
   static constexpr int COPY = K * 1024;              // bytes between a thread's copies
   const Lut8Args& a;

@@ -441,9 +441,23 @@ int64_t route_positions(int64_t T, int ntask) { return T + (int64_t)ntask * (KS 
 
 size_t pad256(size_t b) { return (b + 255) / 256 * 256; }
 
+// Several LUT sets: whole groups per pair, whose bins go to dlut without partial bins,
+// while that leaves at most a tenth of the last round idle.
+bool whole_groups(int64_t n, int64_t d, int gpr, int ntask) {
+  if (d / gpr % TN != 0) return false;
+  const int64_t units = (int64_t)ntask * gpr * gemm::tiles_of(n), pairs = num_sms() / 2;
+  return 10 * units >= 9 * ((units + pairs - 1) / pairs * pairs);
+}
+
+// Otherwise the sets go in blocks whose partial bins take kPartBytes at most (one
+// set's if that is more): they grow with n d and the sets, whatever the tokens are
+// (256 sets of 4-bit indices at 11008 x 4096 would take 6 GB).
+constexpr size_t kPartBytes = size_t(512) << 20;
+
 struct Layout {
   size_t perm, segs, dy, x, part, extra, total;
   int64_t rows;
+  int sets;                // LUT sets per launch
 };
 
 size_t part_floats(int64_t n, int64_t d, int bits, int gpr) {
@@ -463,7 +477,15 @@ Layout layout(int64_t n, int64_t d, int bits, int gpr, int64_t T, int ntask, boo
   l.segs = take(routed ? (size_t)ntask * 8 : 0);
   l.dy = take(routed ? (size_t)l.rows * n * 2 : 0);
   l.x = take((size_t)l.rows * d * 2);
-  l.part = take((routed ? ntask : 1) * part_floats(n, d, bits, gpr) * 4);
+  const size_t one = part_floats(n, d, bits, gpr) * 4;
+  l.sets = routed ? ntask : 1;
+  if (routed && whole_groups(n, d, gpr, ntask)) {
+    l.part = at;
+  } else {
+    const size_t fit = kPartBytes / one;
+    if ((size_t)l.sets > fit) l.sets = fit < 1 ? 1 : (int)fit;
+    l.part = take(l.sets * one);
+  }
   // the parts of the cut round beyond each tile's first
   gemm::Shape shape = gemm::shape_of(n, d, T);
   gemm::split_last_round(shape);
@@ -560,7 +582,6 @@ cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* sca
   cudaError_t e;
   const Layout l = layout(p.n, p.d, p.bits, p.gpr, p.T, p.ntask, routed);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const int sets = routed ? p.ntask : 1;
   int* segs = nullptr;
   uint16_t* X = reinterpret_cast<uint16_t*>(ws + l.x);
   const uint16_t* a_rows = dY;
@@ -600,11 +621,9 @@ cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* sca
   args.gs = p.gs;
   args.gpr = p.gpr;
   args.slots = group_slots(p.gs, p.gpr);
-  args.sets = sets;
   args.part = reinterpret_cast<float*>(ws + l.part);
   args.part_set_stride = (int64_t)part_floats(p.n, p.d, p.bits, p.gpr);
   args.extra = reinterpret_cast<float*>(ws + l.extra);
-  args.segs = segs;
   args.check = p.check;
   const int64_t per_set = p.n * p.gpr * (1 << p.bits);
   // without task ids the sets beyond the first have no tokens
@@ -612,33 +631,41 @@ cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* sca
     e = cudaMemsetAsync(dlut + per_set, 0, (size_t)per_set * (p.ntask - 1) * 4, s);
     if (e != cudaSuccess) return e;
   }
-  int64_t count = routed ? (int64_t)sets * args.shape.mt * args.shape.nt : gemm::items(args.shape);
-  if (routed && p.gs % TN == 0) {
-    // whole groups per pair while that leaves at most a tenth of the last round idle
-    const int64_t units = (int64_t)sets * p.gpr * args.shape.mt, pairs = num_sms() / 2;
-    if (10 * units >= 9 * ((units + pairs - 1) / pairs * pairs)) {
-      args.per_group = (int)(p.gs / TN);
-      args.dlut = dlut;
-      args.accumulate = accumulate;
-      count = units;
-    }
+  const bool grouped = routed && whole_groups(p.n, p.d, p.gpr, p.ntask);
+  if (grouped) {
+    args.per_group = (int)(p.gs / TN);
+    args.accumulate = accumulate;
   }
-  const int64_t quads = per_set * sets / 4;
   const bool cut = args.shape.split > 1;
-  auto go = [&](auto bits) {
+  // a block of LUT sets; the next one's partial bins take the same room after it
+  auto go = [&](auto bits, int first, int sets) {
     constexpr int B = decltype(bits)::value;
+    args.sets = sets;
+    args.segs = routed ? segs + 2 * first : nullptr;
+    args.dlut = dlut + first * per_set;
+    const int64_t count = grouped  ? (int64_t)sets * p.gpr * args.shape.mt
+                          : routed ? (int64_t)sets * args.shape.mt * args.shape.nt
+                                   : gemm::items(args.shape);
     cudaError_t err = gemm::launch_pairs<8, stages(B)>(lut8_tc_kernel<B>, count, s, tm_dy, tm_x, args);
-    if (err != cudaSuccess || args.per_group) return err;
+    if (err != cudaSuccess || grouped) return err;
+    const int64_t quads = per_set * sets / 4;
     const unsigned grid = (unsigned)((quads + 255) / 256);
-    if (cut) lut8_reduce_kernel<B, true><<<grid, 256, 0, s>>>(args, reinterpret_cast<float4*>(dlut), accumulate, quads);
-    else lut8_reduce_kernel<B, false><<<grid, 256, 0, s>>>(args, reinterpret_cast<float4*>(dlut), accumulate, quads);
+    float4* out = reinterpret_cast<float4*>(args.dlut);
+    if (cut) lut8_reduce_kernel<B, true><<<grid, 256, 0, s>>>(args, out, accumulate, quads);
+    else lut8_reduce_kernel<B, false><<<grid, 256, 0, s>>>(args, out, accumulate, quads);
     return cudaGetLastError();
   };
-  switch (p.bits) {
-    case 2: return go(std::integral_constant<int, 2>());
-    case 3: return go(std::integral_constant<int, 3>());
-    default: return go(std::integral_constant<int, 4>());
+  const int all = routed ? p.ntask : 1;
+  for (int first = 0; first < all; first += l.sets) {
+    const int sets = all - first < l.sets ? all - first : l.sets;
+    switch (p.bits) {
+      case 2: e = go(std::integral_constant<int, 2>(), first, sets); break;
+      case 3: e = go(std::integral_constant<int, 3>(), first, sets); break;
+      default: e = go(std::integral_constant<int, 4>(), first, sets); break;
+    }
+    if (e != cudaSuccess) return e;
   }
+  return cudaSuccess;
 }
 
 cudaError_t launch_lut8_simt(const Problem& p, const int8_t* q, const uint8_t* scale, const uint16_t* dY, float* dlut,

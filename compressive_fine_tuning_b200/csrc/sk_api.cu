@@ -148,16 +148,24 @@ bool routed_dx_possible(int64_t n, int64_t d, int64_t T, int ntask) {
 // tensor cores win falls with the layer's size, since their time hardly depends on a
 // few tokens: measured 11 us against 10.7 (CUDA cores) at n x d = 256 x 512 and 16
 // tokens, 25.3 against 25.1 at 4096 x 4096 and 4, 45 against 43 at 8192 x 5120 and 1.
-// With several LUT sets the tensor cores bin n d values for each, the CUDA cores only
-// for those that a token names: with three sets 63.5 against 62.6 at 4096 x 4096 and 8
-// tokens, 126 against 127 at 8192 x 5120 and 8, 18.9 against 19.8 at 1024 x 1024 and
-// 15; with eight 128 against 148 at 4096 x 4096 and 15, 127 against 90 at 8.
-bool use_tensor_cores_lut8(int64_t n, int64_t d, int64_t T, int ntask) {
+// With several LUT sets the tensor cores bin n d values for each, named or not, the
+// CUDA cores only those of sets that a token names, a warp per row and group, in which
+// groups below 1024 columns leave lanes idle and small layers wait for loads.
+// Measured (tensor cores against CUDA cores, us): three sets 73 against 66 at 4096 x
+// 4096 and 8 tokens, eight sets 108 against 109 there and 12; at 4096 x 4096 in four
+// groups 64 sets 718 against 528 and 40 tokens, 720 against 672 and 64, 256 sets 2764
+// against 1832 and 102, 2792 against 2879 and 192; in eight groups 64 sets 673 against
+// 844 and 40, 256 sets 2582 against 1826 and 64, 2618 against 3423 and 128; at 1024 x
+// 1024 in four 256 sets 243 against 129 and 16, 249 against 309 and 64.
+bool use_tensor_cores_lut8(int64_t n, int64_t d, int gpr, int64_t T, int ntask) {
   if (ntask > sk::kMaxRouteTasks) return false;
   const int forced = env_path("SK_BWD_PATH");
   if (forced == 1) return false;
-  if (forced == 2 || T >= 16) return true;
-  return ntask > 1 ? T >= 6 + ntask : T * n * d >= (int64_t(1) << 26);
+  if (forced == 2) return true;
+  if (ntask == 1) return T >= 16 || T * n * d >= (int64_t(1) << 26);
+  if (T < 16) return T >= 6 + ntask;
+  const double lanes = (double)(d / gpr) / 1024.0, size = std::sqrt((double)n * (double)d) / 4096.0;
+  return (double)T >= 0.6 * ntask * (lanes < 1.0 ? lanes : 1.0) * (size < 1.0 ? size : 1.0);
 }
 
 // Shape rules shared by the layer calls.
@@ -284,7 +292,7 @@ size_t sk_workspace_bytes(int op, int64_t n, int64_t d, int bits, int gpr, int64
   if (op == SK_OP_BWD_INPUT && routed_dx_possible(n, d, T, ntask)) return sk::dx_tc_workspace(T, n, ntask);
   if (op == SK_OP_BWD_LUT && routed_dx_possible(n, d, T, ntask))
     return sk::dlut_tc_routed_workspace(n, d, bits, gpr, T, ntask);
-  if (op == SK_OP_BWD_LUT_CKPT8 && use_tensor_cores_lut8(n, d, T, ntask))
+  if (op == SK_OP_BWD_LUT_CKPT8 && use_tensor_cores_lut8(n, d, gpr, T, ntask))
     return sk::lut8_tc_workspace(n, d, bits, gpr, T, ntask);
   return 0;
 }
@@ -612,7 +620,7 @@ sk_status sk_linear_bwd_lut_ckpt8(const void* packed, int bits, int gpr, int64_t
   if (ntask == 1) task = nullptr;
   sk::Problem p = make_problem(packed, nullptr, bits, gpr, n, d, T, task, ntask, check);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = use_tensor_cores_lut8(n, d, T, ntask)
+  cudaError_t e = use_tensor_cores_lut8(n, d, gpr, T, ntask)
                       ? sk::launch_lut8_tc(p, q, scale, dY, dlut, accumulate, task != nullptr, workspace, s)
                       : sk::launch_lut8_simt(p, q, scale, dY, dlut, accumulate, s);
   return e == cudaSuccess ? ok() : cuda_fail(e, "LUT-gradient kernel launch");

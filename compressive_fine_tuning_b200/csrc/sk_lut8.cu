@@ -513,25 +513,34 @@ __global__ void __launch_bounds__(kBlock) lut8_simt_kernel(Problem p, const int8
   if (wid >= p.n * p.gpr) return;
   const int64_t i = wid / p.gpr, g = wid % p.gpr;
   const int64_t cpg = p.gs / 32, chunks = p.d / 32;
-  // a few tokens name few of the sets: the others get zeros (without task ids every
-  // token belongs to LUT set 0)
+  // Of several sets a warp visits the tokens of each by ballots over 32 ids at a time,
+  // so that what a set costs beside its own tokens is an id per lane and 32 tokens.
+  // (A look at every token's id for every set: 9.7 ms for 64 tokens of 256 sets at
+  // 4096 x 4096, 1.1 this way.)  Sets that no token names get zeros; without task ids every token
+  // belongs to LUT set 0.
   const int own = p.task != nullptr && lane < p.T ? token_task(p.task, lane, p.ntask, p.check) : -1;
+  auto named = [&](int64_t b, int tau) {               // tokens b .. b + 31 of the set
+    const int id = b == 0 ? own : b + lane < p.T ? token_task(p.task, b + lane, p.ntask, p.check) : -1;
+    return __ballot_sync(0xffffffffu, id == tau);
+  };
   for (int tau = 0; tau < p.ntask; ++tau) {
-    const bool any = p.task == nullptr ? tau == 0 : p.T > 32 || __any_sync(0xffffffffu, own == tau);
+    bool any = p.task == nullptr && tau == 0;
+    if (p.task != nullptr)
+      for (int64_t b = 0; b < p.T && !any; b += 32) any = named(b, tau) != 0u;
     if (!any) {
       if (lane < K && !accumulate) dlut[(((int64_t)tau * p.n + i) * p.gpr + g) * K + lane] = 0.f;
       continue;
     }
 #pragma unroll
     for (int c = 0; c < K; ++c) bins[c][tid] = 0.f;
-    for (int64_t cc = lane; cc < cpg; cc += 32) {
-      const int64_t chunk = g * cpg + cc;
+    for (int64_t c0 = 0; c0 < cpg; c0 += 32) {         // the whole warp: the ballots are its own
+      const bool mine = c0 + lane < cpg;
+      const int64_t chunk = g * cpg + (mine ? c0 + lane : 0);
       const Chunk<BITS> ch = load_chunk<BITS>(p.packed + i * p.row_bytes, chunk);
       float G[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) G[e] = 0.f;
-      for (int64_t t = 0; t < p.T; ++t) {
-        if (p.task != nullptr && token_task(p.task, t, p.ntask, p.check) != tau) continue;
+      auto add = [&](int64_t t) {
         const uint32_t s2 = __ldg(dY + t * p.n + i);
         const uint32_t sc = ckpt8_scale2(__ldg(scale + t * chunks + chunk));
         const uint4* xp = reinterpret_cast<const uint4*>(q + t * p.d + chunk * 32);
@@ -547,7 +556,15 @@ __global__ void __launch_bounds__(kBlock) lut8_simt_kernel(Problem p, const int8
             fma_bf16x2_scalar(w1, s2, G[16 * h + 4 * b + 2], G[16 * h + 4 * b + 3]);
           }
         }
+      };
+      if (p.task == nullptr) {
+        if (mine)
+          for (int64_t t = 0; t < p.T; ++t) add(t);
+      } else {
+        for (int64_t b = 0; b < p.T; b += 32)
+          for (uint32_t left = named(b, tau); left != 0u && mine; left &= left - 1u) add(b + __ffs(left) - 1);
       }
+      if (!mine) continue;
 #pragma unroll
       for (int e = 0; e < 32; ++e) bins[chunk_index<BITS>(ch, e)][tid] += G[e];
     }

@@ -869,14 +869,17 @@ def sketched_linear(X: torch.Tensor, lut: torch.Tensor, packed: torch.Tensor, bi
     gradient is rounded to fp16).  lut16: the fp16 tables of an fp32 master,
     when the caller keeps them (else they are rounded from `lut` here).
     ckpt: keep X in 8 bits for the LUT gradient, either a Ckpt8 of X that the
-    caller has (layers that share an input share it) or True to make one here."""
+    caller has (layers that share an input share it) or True to make one here;
+    without grad mode nothing is kept and none is made."""
     if lut16 is None:
         lut16 = lut if lut.dtype == torch.float16 else lut.detach().to(torch.float16)
     if ckpt is not False and ckpt is not None:
         q, scale = (None, None) if ckpt is True else ckpt
         if q is not None and tuple(q.shape) != tuple(X.shape):
             raise ValueError("the checkpoint must have X's shape")
-        return SketchedLinearCkpt8Function.apply(_rows(X), lut, lut16, packed, bits, task, q, scale)
+        X = _rows(X)
+        if torch.is_grad_enabled():
+            return SketchedLinearCkpt8Function.apply(X, lut, lut16, packed, bits, task, q, scale)
     return SketchedLinearFunction.apply(X, lut, lut16, packed, bits, task)
 
 

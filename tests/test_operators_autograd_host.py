@@ -63,3 +63,43 @@ def test_backward_passes_refuse_a_tangent_of_the_incoming_gradient(stubs):
         for out, leaf in ((y, x), (loss, h)):
             with pytest.raises(NotImplementedError):
                 torch.autograd.grad(out, leaf, fwad.make_dual(torch.ones(out.shape), torch.ones(out.shape)))
+
+
+# ---- the layer that keeps its input in 8 bits --------------------------------------
+
+@pytest.fixture
+def layer(monkeypatch):
+    """A SketchedLinear on the CPU, and the calls that it makes."""
+    calls = []
+
+    def fwd(packed, lut, bits, X, task=None, **kw):
+        calls.append("fwd")
+        return torch.zeros((X.shape[0], lut.shape[1]), dtype=torch.bfloat16)
+
+    def ckpt8(X):
+        calls.append("ckpt8")
+        return sk.Ckpt8(torch.zeros(X.shape, dtype=torch.int8),
+                        torch.zeros((X.shape[0], X.shape[1] // 32), dtype=torch.uint8))
+
+    monkeypatch.setattr(sk, "linear_fwd", fwd)
+    monkeypatch.setattr(sk, "ckpt8", ckpt8)
+    packed = torch.zeros((64, sk.packed_row_bytes(96, 4)), dtype=torch.uint8)
+    return sk.SketchedLinear(packed, torch.zeros(1, 64, 3, 16), 4, 96, ckpt8=True), calls
+
+
+def _x(T=5, d=96, grad=True):
+    return torch.randn(T, d).to(torch.bfloat16).requires_grad_(grad)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_no_checkpoint_is_made_where_no_gradient_follows(layer, mode):
+    m, calls = layer
+    with mode():
+        m(_x())
+    assert calls == ["fwd"]
+    m.lut.requires_grad_(False)
+    m(_x())
+    assert calls == ["fwd"] * 2
+    m.lut.requires_grad_(True)
+    m(_x(grad=False))
+    assert calls == ["fwd"] * 3 + ["ckpt8"]

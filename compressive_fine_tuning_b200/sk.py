@@ -493,6 +493,22 @@ def _need_ckpt8(ck: "Ckpt8"):
     return q, scale, T, d
 
 
+def _ckpt8_for(X: torch.Tensor, ck: Ckpt8):
+    """(q, scale) of a checkpoint that a caller has of X, as the backward pass will
+    want them: a wrong one is refused before the forward pass, a part of a longer
+    batch's one is brought to the library's alignment."""
+    q, scale = ck
+    if not isinstance(q, torch.Tensor) or q.dtype != torch.int8 or not isinstance(scale, torch.Tensor) \
+            or scale.dtype != torch.uint8:
+        raise TypeError("a checkpoint is an int8 and a uint8 tensor")
+    if q.dim() != 2 or q.shape != X.shape:
+        raise ValueError("the checkpoint must have X's shape")
+    if q.shape[1] % 32 or scale.shape != (q.shape[0], q.shape[1] // 32):
+        raise ValueError("scale must hold one byte per 32 columns of q")
+    _together(X, q, scale)
+    return _rows(q), _rows(scale)
+
+
 def ckpt8(X: torch.Tensor) -> Ckpt8:
     """The 8-bit checkpoint of bf16 rows X [T, d] (d a multiple of 32)."""
     _need(X, torch.bfloat16, "X", 2)
@@ -874,9 +890,7 @@ def sketched_linear(X: torch.Tensor, lut: torch.Tensor, packed: torch.Tensor, bi
     if lut16 is None:
         lut16 = lut if lut.dtype == torch.float16 else lut.detach().to(torch.float16)
     if ckpt is not False and ckpt is not None:
-        q, scale = (None, None) if ckpt is True else ckpt
-        if q is not None and tuple(q.shape) != tuple(X.shape):
-            raise ValueError("the checkpoint must have X's shape")
+        q, scale = (None, None) if ckpt is True else _ckpt8_for(X, ckpt)
         X = _rows(X)
         if torch.is_grad_enabled():
             return SketchedLinearCkpt8Function.apply(X, lut, lut16, packed, bits, task, q, scale)

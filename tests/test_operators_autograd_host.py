@@ -103,3 +103,56 @@ def test_no_checkpoint_is_made_where_no_gradient_follows(layer, mode):
     m.lut.requires_grad_(True)
     m(_x(grad=False))
     assert calls == ["fwd"] * 3 + ["ckpt8"]
+
+
+def _ck(T=5, d=96, q=torch.int8, scale=torch.uint8, groups=None, device="cpu"):
+    return sk.Ckpt8(torch.zeros((T, d), dtype=q, device=device),
+                    torch.zeros((T, groups if groups is not None else d // 32), dtype=scale, device=device))
+
+
+@pytest.mark.parametrize("mode", [contextlib.nullcontext, torch.no_grad])
+@pytest.mark.parametrize("ck,error", [
+    (_ck(T=4), ValueError), (_ck(d=64), ValueError), (_ck(groups=4), ValueError), (_ck(groups=0), ValueError),
+    (_ck(q=torch.uint8), TypeError), (_ck(scale=torch.int8), TypeError), (_ck(q=torch.float32), TypeError),
+    (sk.Ckpt8(_ck().q, _ck(T=6).scale), ValueError), (_ck(device="meta"), ValueError),
+    (sk.Ckpt8(_ck().q, _ck(device="meta").scale), ValueError), (sk.Ckpt8(_ck().q, None), TypeError)])
+def test_a_checkpoint_that_does_not_fit_is_refused_before_the_forward_pass(layer, mode, ck, error):
+    m, calls = layer
+    with mode(), pytest.raises(error):
+        m(_x(), None, ck)
+    assert not calls
+
+
+def test_a_part_of_a_checkpoint_is_taken(layer, monkeypatch):
+    """Rows of a longer batch's checkpoint: their scales start at any byte."""
+    m, calls = layer
+    whole = sk.Ckpt8(torch.arange(9 * 96).to(torch.int8).reshape(9, 96), torch.arange(27).to(torch.uint8).reshape(9, 3))
+    part = sk.Ckpt8(whole.q[2:7], whole.scale[2:7])
+    assert part.scale.data_ptr() % 16
+    got = []
+
+    def bwd(packed, bits, gpr, ck, dY, task=None, ntask=1, **kw):
+        got.append(ck)
+        return torch.zeros((ntask, 64, gpr, 16))
+
+    monkeypatch.setattr(sk, "linear_bwd_lut_ckpt8", bwd)
+    m(_x(grad=False), None, part).backward(torch.ones((5, 64), dtype=torch.bfloat16))
+    assert calls == ["fwd"]
+    assert torch.equal(got[0].q, part.q) and torch.equal(got[0].scale, part.scale)
+    assert got[0].q.data_ptr() % 16 == 0 and got[0].scale.data_ptr() % 16 == 0
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_the_layer_keeps_its_input_in_8_bits_only(layer, own):
+    m, _ = layer
+    saved = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: saved.append(t) or t, lambda t: t):
+        m(_x(), None, _ck() if own else None)
+    kept = [t for t in saved if t.dim() == 2 and t.shape[0] == 5]
+    assert sorted(str(t.dtype) for t in kept) == ["torch.int8", "torch.uint8"]
+    assert sum(t.numel() * t.element_size() for t in kept) == 5 * 96 * 33 // 32
+    m.lut.requires_grad_(False)                         # and none where only X's gradient is wanted
+    saved.clear()
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: saved.append(t) or t, lambda t: t):
+        m(_x(), None, _ck() if own else None)
+    assert not [t for t in saved if t.dim() == 2 and t.shape[0] == 5]

@@ -9,7 +9,9 @@
 //
 // Every value is computed in fp32 and rounded once.  The variance is the mean
 // square of the centred values (two passes over registers), so a row whose mean
-// is far larger than its spread loses nothing.
+// is far larger than its spread loses no more than the rounding of that mean (a few
+// 2^-24 of it), which 16-bit rows do not notice.  rstd is 1 / sqrtf in the kernels of one row
+// and rsqrtf (2 steps of 2^-23 at most) in those of two, and the sums' orders differ between them.
 //
 // Both directions are bound by memory: 2 values of traffic per element forward,
 // 4 over both directions.  A team of threads (one warp for short rows, one CTA
@@ -983,8 +985,10 @@ cudaError_t fwd_shape(const NormFwd& a, cudaStream_t s) {
       };
       // Rows that the threads cover exactly, nothing to check: 26.7 against 29.7 us at
       // [8192, 4096], and 30.2 against 34.3 at [4096, 5120] of a layer norm with a checkpoint.
-      // An RMS norm with a checkpoint is slower so (27.7 against 25.4 us at [4096, 5120]: the
-      // compiler moves more ahead, into registers) and keeps the checks.
+      // An RMS norm with a checkpoint keeps the checks: without them the compiler moves more
+      // ahead (121 registers against 94: three CTAs of 160 threads per SM instead of four, 26.1
+      // against 24.0 us at [4096, 5120]) and gains a little elsewhere (18.5 against 18.9 at [4096, 4096], 21.5
+      // against 22.4 at [2048, 8192], 36.0 against 38.1 at [4096, 7168]).
       const bool full = a.d == (int64_t)th * 8 * pair_chunks<T>();
       auto shape = [&](auto rms, auto bias) {
         constexpr bool RMS = decltype(rms)::value, BIAS = decltype(bias)::value;

@@ -752,7 +752,8 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
     A reduced loss's gradient is known up to one factor, so the forward pass
     computes loss and gradients together (the logits' product is not repeated)
     and the backward pass scales them in place by the incoming gradient, which a
-    factor of 1 leaves alone.  They are handed out once; a second backward pass
+    factor of 1 leaves alone and a power of two scales exactly; any other factor (a
+    loss divided by three) rounds them to bf16 a second time.  They are handed out once; a second backward pass
     over a retained graph computes them again, as does reduction "none", whose
     gradient needs every token's factor.  So does a backward pass that is captured
     into a CUDA graph without its forward pass: its replays would scale the same

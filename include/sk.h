@@ -278,10 +278,16 @@ sk_status sk_linear_bwd_lut_noalloc(const void* packed, int bits, int gpr, int64
  * sk_ckpt8_dequantize: q, scale -> X (bf16 [T][d]), the values the block stands for.
  *
  * sk_linear_bwd_lut_ckpt8: sk_linear_bwd_lut with X given as a checkpoint: the
- * gradient for the values that it stands for, without a bf16 copy of X.  Shape
+ * gradient for the values that it stands for.  Shape
  * rules, task rules and errors are those of sk_linear_bwd_lut; the workspace is
  * sk_workspace_bytes(SK_OP_BWD_LUT_CKPT8, ...) bytes when that is not 0 and is
- * required then.  With one LUT set every token belongs to it and task is not read.
+ * required then.  What a checkpoint saves it saves between the forward and the
+ * backward pass: while the tensor cores form the gradient, the workspace holds X in
+ * bf16 (2 T d bytes), with several LUT sets a copy of dY in task order as well (2 T n
+ * bytes, and up to 63 rows more of both per set), and partial bins: those of one
+ * LUT set or, with several, of as many at a time as fit 512 MiB.  Few tokens take the
+ * CUDA cores, whose workspace is 0.
+ * With one LUT set every token belongs to it and task is not read.
  * Deterministic, with several LUT sets too.
  */
 sk_status sk_ckpt8_quantize(const uint16_t* X, int64_t T, int64_t d, int8_t* q, uint8_t* scale, sk_stream_t stream);
@@ -334,18 +340,23 @@ sk_status sk_layer_norm_bwd(const void* dy, const void* x, int xtype, int64_t T,
  * NULL when only gradients are wanted.
  * dH (bf16 [T][d]) and dW (bf16 [V][d]): the gradients, each NULL when it is not
  * wanted.  dloss: the gradient of the result, fp32 on the device, [T] with
- * SK_CE_NONE and [1] otherwise; NULL means ones.  Probabilities are rounded to
- * bf16 for the two gradient products, sums are fp32.
+ * SK_CE_NONE and [1] otherwise; NULL means ones.  Probabilities are held in 16 bits
+ * (2^-11 of each down to 2^-29 of the largest of its 128 or 256 neighbouring classes,
+ * 2^-40 of that one below) and rounded to bf16 for the two gradient products, sums are
+ * fp32.  What that rounding takes off p - 1 at the target is given back in dH, not in dW.
  * target, loss and dloss need only the alignment of their own values.
  * 1 <= V < 2^24, 8 <= d < 2^20, d % 8 == 0.  T == 0: a reduced loss is 0, dW is
  * zeroed.  workspace: sk_cross_entropy_workspace_bytes(T, V, d, dH != NULL,
  * dW != NULL) bytes; with gradients it holds one chunk of tokens' exponentials
  * (512 MiB at most, or 256 tokens' if that is more), and for dW the room of the
- * chunk's rows of H.  Deterministic.
+ * chunk's rows of H and, with more tokens than one chunk has, dW's sums in fp32 (4 V d
+ * bytes).  Deterministic.
  *
  * sk_scale_bf16: x (bf16 [nx]) and y (bf16 [ny]; sizes multiples of 8, either may be
  * 0) times the device scalar *factor, in place, in one launch; a factor of exactly
- * 1 leaves them alone.  For the gradients of a loss that something scales afterwards.
+ * 1 leaves them alone.  For the gradients of a loss that something scales afterwards:
+ * any other factor than a power of two rounds them to bf16 a second time, which a
+ * dloss given to sk_cross_entropy does not.
  */
 size_t sk_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t d, int want_dh, int want_dw);
 sk_status sk_cross_entropy(const uint16_t* H, const uint16_t* W, const void* target, int target_bits, int64_t T,

@@ -4,6 +4,10 @@
 //   l = H W^T,  lse_t = log sum_v exp(l_tv),  loss_t = lse_t - l_t,target
 //   P = c_t (softmax(l_t) - onehot(target)),  dH = P W,  dW = P^T H
 //
+// (c is taken apart into one number per chunk of tokens, which multiplies the
+// products' fp32 sums, and P's own part: 1 of a reduced loss, the weight over the
+// chunk's largest of per-token losses).
+//
 // The loss alone is one product whose epilogue reduces every 256-column tile of
 // a row to its largest logit and its sum of exponentials; a second kernel joins
 // a row's tiles.  Nothing else is written.
@@ -24,10 +28,12 @@
 // the same tile was 6 % off, one 18 below it lost.)  P is rounded to bf16 for the
 // products (2^-8 of each value at most).  The target's entry does not come
 // from the buffer: p - 1 is formed from the fp32 loss as expm1(-loss), so a
-// token that is already predicted surely keeps its small gradient's precision.
-// What its bf16 rounding takes off is given back in dH, whose rows have one target
+// token that is already predicted surely keeps its small gradient's precision, down
+// to the 2^-24 that a sum of exponentials next to 1 is rounded to.  What its bf16 rounding takes off is given back in dH, whose rows have one target
 // each; in dW, where any number of tokens share a row, it stays (1e-3 of dW at 8192
-// tokens and 32000 classes, where rounding dW to bf16 takes 1.7e-3).
+// tokens and 32000 classes, where rounding dW to bf16 takes 1.7e-3).  A factor that
+// tokens share is kept out of that rounding: 1 / 8160 in P, halfway between two bf16
+// values, moved all of dW by 2^-8.
 //
 // The bound is the tensor pipe: 2 T V d flops per product.
 #include <type_traits>
@@ -167,12 +173,17 @@ struct Shared {
   unsigned long long count;   // tokens that take part
   unsigned int blocks;        // blocks of lse_kernel that are done
   unsigned int dirty;         // a token that takes no part has a NaN or an infinity in its row of H
+  unsigned int top;           // fp32 bits of the largest weight of a token that takes part (per-token losses)
 };
+
+// The shared part of per-token weights.
+__device__ __forceinline__ float top_weight(const Shared* s) { return s->top != 0 ? __uint_as_float(s->top) : 1.f; }
 
 __device__ __forceinline__ void start_chunk(Shared* s, int keep_count) {
   if (blockIdx.x != 0 || threadIdx.x != 0) return;
   s->blocks = 0;
   s->dirty = 0;
+  s->top = 0;
   if (!keep_count) s->count = 0;
 }
 
@@ -397,10 +408,25 @@ struct GradOut {
   int add, last;
   int64_t M, N;
   TargetRest rest;
+  const float* dloss;       // the factor of a reduced loss, or nullptr (one)
+  const Shared* count;      // divide by its count (mean), or nullptr
+  const Shared* top;        // the factor of per-token losses with weights, or nullptr
+
+  // What the products' sums are multiplied by: 0 for dH's rows of tokens that take no
+  // part, whatever the factor is.
+  __device__ __forceinline__ float scale(const uint16_t* wrow) const {
+    if (rest.rest != nullptr && wrow == nullptr) return 0.f;
+    if (top != nullptr) return top_weight(top);
+    const float c = dloss != nullptr ? __ldg(dloss) : 1.f;
+    return count != nullptr ? c / (float)(count->count > 0 ? count->count : 1) : c;
+  }
 
   // eight columns of a row (N % 8 == 0: inside or outside as a whole)
-  __device__ __forceinline__ void finish(float (&f)[8], int64_t row, int64_t col, const uint16_t* wrow, float r) const {
+  __device__ __forceinline__ void finish(float (&f)[8], int64_t row, int64_t col, const uint16_t* wrow, float r,
+                                         float c) const {
     if (wrow != nullptr) add_scaled8(f, wrow + col, r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= c;
     if (acc != nullptr) {
       float4* p = reinterpret_cast<float4*>(acc + row * N + col);
 #pragma unroll
@@ -436,6 +462,7 @@ struct GradEpi {
     const int64_t row = m0 + 32 * warp + lane;
     float r = 0.f;
     const uint16_t* wrow = part < 0 && row < o.M ? o.rest.row(row, r, check) : nullptr;
+    const float c = o.scale(wrow);
 #pragma unroll 1
     for (int h = 0; h < gemm::TN / 64; ++h) {
       const int c0 = n0 + 64 * h;
@@ -460,7 +487,7 @@ struct GradEpi {
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * j + e]);
           const int64_t col = c0 + 32 * q + 8 * j;
-          if (row < o.M && col < o.N) o.finish(f, row, col, wrow, r);
+          if (row < o.M && col < o.N) o.finish(f, row, col, wrow, r, c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[16 * q + 4 * j + e] = f32x2_to_bf16x2(f[2 * e], f[2 * e + 1]);
         }
@@ -524,6 +551,7 @@ struct GradTEpi {
       const int64_t t = n0 + k;
       float r = 0.f;
       const uint16_t* wrow = item.part < 0 ? o.rest.row(t, r, check) : nullptr;
+      const float c = o.scale(wrow);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         if (c0 + 8 * g >= o.N) break;
@@ -535,7 +563,7 @@ struct GradTEpi {
           p[0] = make_float4(f[0], f[1], f[2], f[3]);
           p[1] = make_float4(f[4], f[5], f[6], f[7]);
         } else {
-          o.finish(f, t, c0 + 8 * g, wrow, r);
+          o.finish(f, t, c0 + 8 * g, wrow, r, c);
           *reinterpret_cast<uint4*>(out + t * o.N + c0 + 8 * g) =
               make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
                          f32x2_to_bf16x2(f[6], f[7]));
@@ -570,7 +598,7 @@ __global__ void __launch_bounds__(256) join_t_kernel(const __grid_constant__ Gra
     f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
     f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
   }
-  a.out.finish(f, t, col, wrow, r);
+  a.out.finish(f, t, col, wrow, r, a.out.scale(wrow));
   *reinterpret_cast<uint4*>(out + t * a.out.N + col) =
       make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
                  f32x2_to_bf16x2(f[6], f[7]));
@@ -588,6 +616,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ GradA
   if (row >= a.out.M) return;
   float r;
   const uint16_t* wrow = a.out.rest.row(row, r, a.check);
+  const float c = a.out.scale(wrow);
   const float4* p = a.parts + ((int64_t)blockIdx.x * s.split * 2 + blockIdx.y) * 64 * 128 +
                     (16 * blockIdx.z + 8 * half) * 128 + r128;
 #pragma unroll
@@ -600,7 +629,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ GradA
       f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
       f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
     }
-    a.out.finish(f, row, col, wrow, r);
+    a.out.finish(f, row, col, wrow, r, c);
     if (a.out.acc == nullptr || a.out.last)
       *reinterpret_cast<uint4*>(out + row * a.out.N + col) =
           make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
@@ -640,6 +669,7 @@ struct LseArgs {
   int64_t V;
   float* lse;
   float* losses;            // [T] of this chunk, or nullptr
+  const float* weights;     // per-token losses: [T] of this chunk, or nullptr
   Shared* shared;
   int count;                // add this chunk's tokens to the count
   // the reduced loss, written by the last block of the last chunk (else nullptr):
@@ -691,6 +721,13 @@ __global__ void __launch_bounds__(8 * Y) lse_kernel(LseArgs a) {
       a.nll[t] = loss;
       if (a.losses != nullptr) a.losses[t] = loss;
     }
+    if (a.weights != nullptr) {                        // the largest is the same in any order
+      float w = keep ? fabsf(a.weights[t]) : 0.f;
+      if (!(w < INFINITY)) w = 0.f;
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffu, w, off));
+      if (threadIdx.x == 0 && w > 0.f) atomicMax(&a.shared->top, __float_as_uint(w));
+    }
     if (a.count) {
       const int n = __popc(__ballot_sync(0xffu, keep));
       if (threadIdx.x == 0 && n) atomicAdd(&a.shared->count, (unsigned long long)n);
@@ -733,9 +770,8 @@ struct ProbArgs {
   int target64;
   int64_t ignore_index;
   int T, V;
-  const float* dloss;
-  int dloss_each;           // dloss has one value per token
-  const Shared* shared;     // divide by its count (mean), or nullptr
+  const float* dloss;       // one value per token, or nullptr
+  const Shared* shared;     // with dloss: its largest, which the products' sums are multiplied by
   int unit_shift;           // log2 of a stats tile's width in units of eight classes (5 or 4)
   float* rest;              // [T]: P's target entry minus its bf16
   const uint16_t* H;        // with dW: the tokens' rows, and whether one that takes no part is not finite
@@ -769,9 +805,7 @@ __global__ void __launch_bounds__(kProbThreads) prob_kernel(ProbArgs a) {
     }
     return;
   }
-  float c = 1.f;
-  if (a.dloss != nullptr) c = a.dloss[a.dloss_each ? t : 0];
-  if (a.shared != nullptr) c /= (float)(a.shared->count > 0 ? a.shared->count : 1);
+  const float c = a.dloss != nullptr ? a.dloss[t] / top_weight(a.shared) : 1.f;
   const float z = a.lse[t];
   const float at_target = c * expm1f(-a.nll[t]);
   if (threadIdx.x == 0) a.rest[t] = at_target - __bfloat162float(__float2bfloat16_rn(at_target));
@@ -1010,16 +1044,19 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
     }
     const int stat_tiles = score ? 2 * shape.mt : exchanged ? (int)((a.V + 127) / 128) : shape.nt;
     const bool reduce = a.reduction != SK_CE_NONE && a.loss != nullptr && t0 + T >= a.T;
+    const bool each = a.reduction == SK_CE_NONE;
+    const float* weights = grads && each && a.dloss != nullptr ? a.dloss + t0 : nullptr;
     LseArgs le{stats, nll, target, a.target64, a.ignore_index, (int)T, stat_tiles, a.V, lse, losses ? losses + t0 : nullptr,
-               shared, mean && !count_first ? 1 : 0, reduce ? a.loss : nullptr, losses, a.T, mean ? 1 : 0, a.check};
+               weights, shared, mean && !count_first ? 1 : 0, reduce ? a.loss : nullptr, losses, a.T, mean ? 1 : 0, a.check};
     // few tokens make few blocks: more threads in each
     if (T <= kScoreTokens) lse_kernel<128><<<(unsigned)((T + 7) / 8), dim3(8, 128), 0, s>>>(le);
     else lse_kernel<32><<<(unsigned)((T + 7) / 8), dim3(8, 32), 0, s>>>(le);
     SK_TRY(cudaGetLastError());
     if (!grads) continue;
-    const bool each = a.reduction == SK_CE_NONE;
+    const float* factor = each ? nullptr : a.dloss;
+    const Shared *count = mean ? shared : nullptr, *top = weights ? shared : nullptr;
     ProbArgs pa{E, l.pitch, stats, lse, nll, target, a.target64, a.ignore_index, (int)T, (int)a.V,
-                each && a.dloss ? a.dloss + t0 : a.dloss, each ? 1 : 0, mean ? shared : nullptr, exchanged ? 4 : 5, rest,
+                weights, shared, exchanged ? 4 : 5, rest,
                 dw ? H : nullptr, a.d, &shared->dirty, a.check};
     prob_kernel<<<(unsigned)T, kProbThreads, 0, s>>>(pa);
     SK_TRY(cudaGetLastError());
@@ -1027,7 +1064,8 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
       CUtensorMap tm_p, tm_dh;
       uint16_t* out = a.dH + t0 * a.d;
       GradArgs ga{gemm::shape_of(T, a.d, a.V),
-                  {nullptr, 0, 1, T, a.d, {rest, a.W, target, a.target64, a.V, a.d, a.ignore_index}}, parts, shared, a.check};
+                  {nullptr, 0, 1, T, a.d, {rest, a.W, target, a.target64, a.V, a.d, a.ignore_index},
+                   factor, count, top}, parts, shared, a.check};
       const int tn = exchanged_tokens(T, gemm::tiles_of(a.d), true);
       if (tn > 0) {
         ga.shape = gemm::shape_of(a.d, T, a.V);
@@ -1059,7 +1097,8 @@ cudaError_t launch_cross_entropy(const CrossEntropy& a, cudaStream_t s) {
           reinterpret_cast<const uint4*>(H), target, a.target64, (int)T, a.V, a.ignore_index, a.d / 8,
           reinterpret_cast<uint4*>(clean), shared, a.check);
       SK_TRY(cudaGetLastError());
-      GradArgs ga{gemm::shape_of(a.V, a.d, T), {acc, t0 > 0 ? 1 : 0, t0 + T >= a.T ? 1 : 0, a.V, a.d, {}}, parts, shared, a.check};
+      GradArgs ga{gemm::shape_of(a.V, a.d, T), {acc, t0 > 0 ? 1 : 0, t0 + T >= a.T ? 1 : 0, a.V, a.d, {}, factor, count, top}, parts,
+                  shared, a.check};
       gemm::split_last_round(ga.shape);
       SK_TRY(gemm::launch_pairs<4, 6>(grad_kernel<1>, gemm::items(ga.shape), s, tm_p, tm_hm, tm_clean, tm_dw, ga));
       SK_TRY(launch_join(ga, a.dW, s));

@@ -342,8 +342,9 @@ sk_status sk_layer_norm_bwd(const void* dy, const void* x, int xtype, int64_t T,
  * wanted.  dloss: the gradient of the result, fp32 on the device, [T] with
  * SK_CE_NONE and [1] otherwise; NULL means ones.  Probabilities are held in 16 bits
  * (2^-11 of each down to 2^-29 of the largest of its 128 or 256 neighbouring classes,
- * 2^-40 of that one below) and rounded to bf16 for the two gradient products, sums are
- * fp32.  What that rounding takes off p - 1 at the target is given back in dH, not in dW.
+ * 2^-40 of that one below) and, times the token's dloss over the largest, rounded to
+ * bf16 for the two gradient products; sums are fp32, and what the tokens' factors have in
+ * common multiplies them.  What that rounding takes off p - 1 at the target is given back in dH, not in dW.
  * target, loss and dloss need only the alignment of their own values.
  * 1 <= V < 2^24, 8 <= d < 2^20, d % 8 == 0.  T == 0: a reduced loss is 0, dW is
  * zeroed.  workspace: sk_cross_entropy_workspace_bytes(T, V, d, dH != NULL,

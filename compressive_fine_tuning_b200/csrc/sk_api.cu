@@ -157,12 +157,13 @@ bool routed_dx_possible(int64_t n, int64_t d, int64_t T, int ntask) {
 // against 1832 and 102, 2792 against 2879 and 192; in eight groups 64 sets 673 against
 // 844 and 40, 256 sets 2582 against 1826 and 64, 2618 against 3423 and 128; at 1024 x
 // 1024 in four 256 sets 243 against 129 and 16, 249 against 309 and 64.
-bool use_tensor_cores_lut8(int64_t n, int64_t d, int gpr, int64_t T, int ntask) {
+// Without task ids (`routed` false) all tokens are one set's, however many there are.
+bool use_tensor_cores_lut8(int64_t n, int64_t d, int gpr, int64_t T, int ntask, bool routed) {
   if (ntask > sk::kMaxRouteTasks) return false;
   const int forced = env_path("SK_BWD_PATH");
   if (forced == 1) return false;
   if (forced == 2) return true;
-  if (ntask == 1) return T >= 16 || T * n * d >= (int64_t(1) << 26);
+  if (ntask == 1 || !routed) return T >= 16 || T * n * d >= (int64_t(1) << 26);
   if (T < 16) return T >= 6 + ntask;
   const double lanes = (double)(d / gpr) / 1024.0, size = std::sqrt((double)n * (double)d) / 4096.0;
   return (double)T >= 0.6 * ntask * (lanes < 1.0 ? lanes : 1.0) * (size < 1.0 ? size : 1.0);
@@ -292,8 +293,15 @@ size_t sk_workspace_bytes(int op, int64_t n, int64_t d, int bits, int gpr, int64
   if (op == SK_OP_BWD_INPUT && routed_dx_possible(n, d, T, ntask)) return sk::dx_tc_workspace(T, n, ntask);
   if (op == SK_OP_BWD_LUT && routed_dx_possible(n, d, T, ntask))
     return sk::dlut_tc_routed_workspace(n, d, bits, gpr, T, ntask);
-  if (op == SK_OP_BWD_LUT_CKPT8 && use_tensor_cores_lut8(n, d, gpr, T, ntask))
-    return sk::lut8_tc_workspace(n, d, bits, gpr, T, ntask);
+  if (op == SK_OP_BWD_LUT_CKPT8) {                   // a call for several sets may come without task ids
+    size_t need = 0;
+    for (bool routed : {false, ntask > 1}) {
+      if (!use_tensor_cores_lut8(n, d, gpr, T, ntask, routed)) continue;
+      const size_t bytes = sk::lut8_tc_workspace(n, d, bits, gpr, T, ntask, routed);
+      if (bytes > need) need = bytes;
+    }
+    return need;
+  }
   return 0;
 }
 
@@ -620,7 +628,7 @@ sk_status sk_linear_bwd_lut_ckpt8(const void* packed, int bits, int gpr, int64_t
   if (ntask == 1) task = nullptr;
   sk::Problem p = make_problem(packed, nullptr, bits, gpr, n, d, T, task, ntask, check);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = use_tensor_cores_lut8(n, d, gpr, T, ntask)
+  cudaError_t e = use_tensor_cores_lut8(n, d, gpr, T, ntask, task != nullptr)
                       ? sk::launch_lut8_tc(p, q, scale, dY, dlut, accumulate, task != nullptr, workspace, s)
                       : sk::launch_lut8_simt(p, q, scale, dY, dlut, accumulate, s);
   return e == cudaSuccess ? ok() : cuda_fail(e, "LUT-gradient kernel launch");

@@ -586,12 +586,8 @@ __global__ void __launch_bounds__(kBlock) lut8_simt_kernel(Problem p, const int8
 
 }  // namespace
 
-size_t lut8_tc_workspace(int64_t n, int64_t d, int bits, int gpr, int64_t T, int ntask) {
-  const size_t one = layout(n, d, bits, gpr, T, ntask, false).total;
-  if (ntask == 1) return one;
-  // a call for several sets may come without task ids: then it is a call for one
-  const size_t several = layout(n, d, bits, gpr, T, ntask, true).total;
-  return one > several ? one : several;
+size_t lut8_tc_workspace(int64_t n, int64_t d, int bits, int gpr, int64_t T, int ntask, bool routed) {
+  return layout(n, d, bits, gpr, T, ntask, routed).total;
 }
 
 cudaError_t launch_lut8_tc(const Problem& p, const int8_t* q, const uint8_t* scale, const uint16_t* dY, float* dlut,

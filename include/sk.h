@@ -286,7 +286,7 @@ sk_status sk_linear_bwd_lut_noalloc(const void* packed, int bits, int gpr, int64
  * bf16 (2 T d bytes), with several LUT sets a copy of dY in task order as well (2 T n
  * bytes, and up to 63 rows more of both per set), and partial bins: those of one
  * LUT set or, with several, of as many at a time as fit 512 MiB.  Few tokens take the
- * CUDA cores, whose workspace is 0.
+ * CUDA cores, which need none (the size covers a call without task ids as well).
  * With one LUT set every token belongs to it and task is not read.
  * Deterministic, with several LUT sets too.
  */

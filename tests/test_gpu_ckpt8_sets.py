@@ -91,3 +91,18 @@ def test_blocks_of_sets(monkeypatch):
     acc = sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, task, sets, out=torch.full_like(got, 0.25), accumulate=True)
     assert torch.equal(acc, 0.25 + got)
     assert sk.device_check() == 0
+
+
+@pytest.mark.parametrize("T", [16, 40, 150])
+def test_many_sets_without_task_ids(T):
+    """All tokens are set 0's: the numbers, and the path, of a call for one set."""
+    from compressive_fine_tuning_b200 import sk
+    n, d, bits, gpr, sets = 520, 1056, 4, 1, 256
+    c = synth.layer_case(60 + T, n=n, d=d, bits=bits, gpr=gpr, T=T)
+    packed, lut, X, dY, _ = gc.dev_case(c)
+    ck = sk.ckpt8(X)
+    whole = sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY)
+    got = sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, None, sets)
+    assert torch.equal(got[0], whole[0]) and not got[1:].any()
+    acc = sk.linear_bwd_lut_ckpt8(packed, bits, gpr, ck, dY, None, sets, out=torch.full_like(got, 0.25), accumulate=True)
+    assert torch.equal(acc, 0.25 + got) and sk.device_check() == 0
